@@ -39,8 +39,9 @@ class Rope:
     def apply(self, positions, q, k=None, q_out=None, k_out=None, inverse: bool = False, stream=None):
         """Rotated (q, k) of [tokens][heads][d_head] tensors (fp32 or bf16, any token and head strides), in one
         launch.  Outputs may be the inputs, and overlap nothing else.  Rows with a negative position are left out:
-        fresh outputs hold a copy of the input there.  ``inverse`` takes the rotation back; it is not recorded for
-        autograd: with magnitude 1 the inputs' gradients are ``apply`` of the outputs' with ``inverse`` flipped."""
+        fresh outputs hold a copy of the input there.  ``inverse`` takes the rotation back.  The call is not recorded
+        for autograd: fresh outputs need no gradient, and a given output that needs one is refused while gradients are
+        recorded.  With magnitude 1 the inputs' gradients are ``apply`` of the outputs' with ``inverse`` flipped."""
         torch = _torch()
         if q.dtype is torch.bfloat16:
             dt = SPECTRA_BF16
@@ -82,13 +83,22 @@ def _pair(name, x, out, T, d, like, st):
         raise TypeError(f"{name} must have q's type and device")
     n = shape[1]
     given = _heads(name, x, n)
-    if out is x:
-        return given, given, out
     if out is None:
-        out = _fresh(x.clone(memory_format=_torch().contiguous_format), st)
-    elif out.shape != shape or out.dtype is not like.dtype or out.get_device() != index:
+        out = _copied(x, st)
+        return given, _heads(name + "_out", out, n), out
+    if out is not x and (out.shape != shape or out.dtype is not like.dtype or out.get_device() != index):
         raise ValueError(f"{name}_out must be like {name}")
-    return given, _heads(name + "_out", out, n), out
+    torch = _torch()
+    if out.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name}_out needs a gradient, which the call does not record")
+    if not out.is_inference():
+        torch.autograd.graph.increment_version(out)  # (a graph may hold it for its backward pass)
+    return given, given if out is x else _heads(name + "_out", out, n), out
+
+
+def _copied(x, st):
+    """A copy of `x` in one row of vectors, unknown to autograd."""
+    return _fresh(x.detach().clone(memory_format=_torch().contiguous_format), st)
 
 
 class AppendPlan:
