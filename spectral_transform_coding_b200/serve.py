@@ -97,8 +97,15 @@ def _pair(name, x, out, T, d, like, st):
 
 
 def _copied(x, st):
-    """A copy of `x` in one row of vectors, unknown to autograd."""
-    return _fresh(x.detach().clone(memory_format=_torch().contiguous_format), st)
+    """A copy of `x` in one row of vectors, made in the call's stream and unknown to autograd."""
+    torch = _torch()
+    x = x.detach()
+    if st.side is None:
+        return x.clone(memory_format=torch.contiguous_format)
+    out = _fresh(torch.empty(x.shape, dtype=x.dtype, device=x.device), st)
+    with torch.cuda.stream(st.side):
+        out.copy_(x)
+    return out
 
 
 class AppendPlan:
