@@ -231,8 +231,9 @@ SPECTRA_API spectra_status spectra_wo_correction(const spectra_codec* codec, int
 /* Workspace bytes for spectra_encode_append with up to max_tokens tokens. */
 SPECTRA_API spectra_status spectra_encode_workspace_bytes(const spectra_codec* codec, int64_t max_tokens,
                                               size_t* bytes);
-/* Workspace bytes for spectra_decode_attend with `batch` sequences of up to
- * max_len tokens. */
+/* Workspace bytes for spectra_decode_attend with `batch` sequences (at most
+ * 65535) of up to max_len tokens.  One workspace serves steps of several batch
+ * sizes if it has the largest of their sizes (a smaller batch may need more). */
 SPECTRA_API spectra_status spectra_decode_workspace_bytes(const spectra_codec* codec, int32_t batch,
                                               int64_t max_len, size_t* bytes);
 
@@ -301,10 +302,14 @@ SPECTRA_API spectra_status spectra_encode_append(const spectra_codec* codec, con
  *   q   device fp32 [batch][n_q_heads][d_head]
  *   out device fp32 [batch][n_q_heads][d_head] (attention output before W_O)
  *   workspace device, >= spectra_decode_workspace_bytes, 256-byte aligned.  It
- *       holds the split-K records and per-(sequence, KV head) arrival counters
- *       that must be zero when a call starts: zero the workspace once before
- *       its first use; every call leaves the counters at zero again.  Calls
- *       that share a workspace must not overlap on the GPU.
+ *       holds per-(sequence, KV head) arrival counters, in its first
+ *       n_kv_heads * 262144 bytes whatever the batch, that must be zero when a
+ *       call starts, and the split-K records behind them: zero the workspace
+ *       once before its first use; every call leaves the counters at zero again,
+ *       so steps of any batch size, of both this call and
+ *       spectra_decode_attend_shared and of any codec with as many KV heads, can
+ *       follow one another.  Calls that share a workspace must not overlap on
+ *       the GPU.
  * q must not be written by a kernel of this library still running in the
  * same stream (q is read before the dependency on earlier launches resolves).
  * A length outside [0, max_pages_per_seq * page_tokens] (that sequence is then
@@ -331,16 +336,16 @@ SPECTRA_API spectra_status spectra_decode_attend(const spectra_codec* codec, con
  * belongs to another framework, code running where an allocation would stall
  * or be refused).  No counterpart on the SPECTRA pages: an interface of this
  * library only.  Arguments as for spectra_decode_attend minus the workspace.
- * The scratch (split-K records and arrival counters) lives in one static 4 MiB
- * device array per GPU, kept until the process exits.  The first call on a
- * device looks up that array's device address (cudaGetSymbolAddress), so make
- * the first call on each device before any stream capture.  Every call shares
- * the array and leaves its contents behind: the counters, which must start at
- * zero, are zero when the library loads and every completed call leaves them
- * at zero; the records are rewritten by each call before they are read.
- * Calls whose kernels can overlap on the GPU (other streams, other codecs at
- * the same time) race on the array: serialise them.  A batch/context
- * whose scratch would exceed 4 MiB fails with SPECTRA_ERR_CAPACITY.  Calls no
+ * The scratch lives in two static device arrays per GPU, 4 MiB of split-K
+ * records and the arrival counters, kept until the process exits.  The first
+ * call on a device looks up their device addresses (cudaGetSymbolAddress), so
+ * make the first call on each device before any stream capture.  Every call
+ * shares the arrays and leaves their contents behind: the counters, which must
+ * start at zero, are zero when the library loads and every completed call
+ * leaves them at zero; the records are rewritten by each call before they are
+ * read.  Calls whose kernels can overlap on the GPU (other streams, other
+ * codecs at the same time) race on the arrays: serialise them.  A batch whose
+ * records would exceed 4 MiB fails with SPECTRA_ERR_CAPACITY.  Calls no
  * cudaMalloc, cudaFree or allocating library routine. */
 SPECTRA_API spectra_status spectra_decode_attend_noalloc(const spectra_codec* codec,
                                                          const spectra_cache* cache, const float* q,
@@ -390,8 +395,8 @@ SPECTRA_API spectra_status spectra_decode_attend_reconstruct(const spectra_codec
 /* Decode for a batch that shares a long prefix                               */
 /* ------------------------------------------------------------------------- */
 
-/* Workspace bytes for spectra_decode_attend_shared with `batch` sequences (any
- * prefix and any lengths). */
+/* Workspace bytes for spectra_decode_attend_shared with `batch` sequences (at
+ * most 65535; any prefix and any lengths). */
 SPECTRA_API spectra_status spectra_decode_shared_workspace_bytes(const spectra_codec* codec, int32_t batch,
                                                                  size_t* bytes);
 
@@ -411,7 +416,8 @@ SPECTRA_API spectra_status spectra_decode_shared_workspace_bytes(const spectra_c
  *       sequence of length 0 (an empty slot of a padded batch) gives 0
  *   workspace device, >= spectra_decode_shared_workspace_bytes(batch), 256-byte
  *       aligned; zero it once before its first use, every call leaves its
- *       counters at zero.  Calls that share a workspace must not overlap.
+ *       counters at zero (as spectra_decode_attend's, which it may share).  Calls
+ *       that share a workspace must not overlap.
  * Precision: over the shared pages latents, folded queries and softmax weights
  * enter the tensor cores as fp16 and every sum is fp32 (see prefix_kernels.cu);
  * dequantised latents and folded queries must fit fp16 (+-65504).  The result is

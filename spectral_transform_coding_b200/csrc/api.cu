@@ -615,8 +615,8 @@ spectra_status spectra_encode_workspace_bytes(const spectra_codec* c, int64_t ma
 spectra_status spectra_decode_workspace_bytes(const spectra_codec* c, int32_t batch, int64_t max_len,
                                               size_t* bytes) {
   if (!c || !bytes || batch <= 0 || max_len < 0) return fail(SPECTRA_ERR_INVALID, "bad arguments");
-  const DecodePlan p = make_decode_plan(c->h, batch, 1 << 30);
-  *bytes = p.ws_bytes;
+  if (batch > kDecodeMaxBatch) return fail(SPECTRA_ERR_UNSUPPORTED, "at most 65535 sequences");
+  *bytes = decode_counter_bytes(c->h) + make_decode_plan(c->h, batch, 1 << 30).rec_bytes;
   return SPECTRA_OK;
 }
 
@@ -695,9 +695,13 @@ spectra_status spectra_decode_attend(const spectra_codec* c, const spectra_cache
   if (s != SPECTRA_OK) return s;
   s = check_device(c);
   if (s != SPECTRA_OK) return s;
+  if (cache->batch > kDecodeMaxBatch) return fail(SPECTRA_ERR_UNSUPPORTED, "at most 65535 sequences");
   const DecodePlan plan = make_decode_plan(c->h, cache->batch, cache->max_pages_per_seq);
-  if (workspace_bytes < plan.ws_bytes) return fail(SPECTRA_ERR_INVALID, "workspace too small");
-  CUDA_TRY(launch_decode(c->h, c->d, *cache, q, out, workspace, plan, static_cast<cudaStream_t>(stream)));
+  const size_t rec_off = decode_counter_bytes(c->h);
+  if (workspace_bytes < rec_off + plan.rec_bytes) return fail(SPECTRA_ERR_INVALID, "workspace too small");
+  CUDA_TRY(launch_decode(c->h, c->d, *cache, q, out, static_cast<int32_t*>(workspace),
+                         reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + rec_off), plan,
+                         static_cast<cudaStream_t>(stream)));
   return SPECTRA_OK;
 }
 
@@ -760,8 +764,8 @@ spectra_status spectra_decode_shared_workspace_bytes(const spectra_codec* c, int
     if (!c->decode_ok) return fail(SPECTRA_ERR_UNSUPPORTED, c->decode_why);
     spectra_status s = check_device(c);
     if (s != SPECTRA_OK) return s;
-    if (batch > kSharedMaxBatch) return fail(SPECTRA_ERR_UNSUPPORTED, "at most 65535 sequences");
-    *bytes = make_shared_plan(c->h, batch).ws_bytes;
+    if (batch > kDecodeMaxBatch) return fail(SPECTRA_ERR_UNSUPPORTED, "at most 65535 sequences");
+    *bytes = decode_counter_bytes(c->h) + make_shared_plan(c->h, batch).rec_bytes;
     return SPECTRA_OK;
   });
 }
@@ -782,11 +786,14 @@ spectra_status spectra_decode_attend_shared(const spectra_codec* c, const spectr
     if ((int64_t)n_prefix * c->cfg.page_tokens > INT32_MAX) return fail(SPECTRA_ERR_INVALID, "prefix too long");
     s = check_device(c);
     if (s != SPECTRA_OK) return s;
-    if (cache->batch > kSharedMaxBatch) return fail(SPECTRA_ERR_UNSUPPORTED, "at most 65535 sequences");
+    if (cache->batch > kDecodeMaxBatch) return fail(SPECTRA_ERR_UNSUPPORTED, "at most 65535 sequences");
     const SharedPlan plan = make_shared_plan(c->h, cache->batch);
-    if (workspace_bytes < plan.ws_bytes) return fail(SPECTRA_ERR_INVALID, "workspace too small");
+    const size_t rec_off = decode_counter_bytes(c->h);
+    if (workspace_bytes < rec_off + plan.rec_bytes) return fail(SPECTRA_ERR_INVALID, "workspace too small");
     CUDA_TRY(launch_decode_shared(c->h, c->d, *cache, static_cast<const uint16_t*>(q), prefix_pages, n_prefix,
-                                  static_cast<uint16_t*>(out), workspace, plan, static_cast<cudaStream_t>(stream)));
+                                  static_cast<uint16_t*>(out), static_cast<int32_t*>(workspace),
+                                  reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + rec_off), plan,
+                                  static_cast<cudaStream_t>(stream)));
     return SPECTRA_OK;
   });
 }
@@ -832,12 +839,16 @@ spectra_status spectra_device_status(const spectra_codec* c, void* stream) {
 // ---------------------------------------------------------------------------
 namespace {
 
-constexpr size_t kStaticScratchBytes = 4u << 20;  // 4 MiB per device
+constexpr size_t kStaticScratchBytes = 4u << 20;  // 4 MiB of split records per device
 static __device__ __align__(256) uint8_t g_static_decode_scratch[kStaticScratchBytes];
+// arrival counters: one for each (sequence, KV head), whose records take 528 bytes at least
+constexpr size_t kStaticCounters = kStaticScratchBytes / 512;
+static __device__ int32_t g_static_decode_counters[kStaticCounters];
 
 struct StaticScratch {
   std::mutex mu;
   void* ptr[64] = {};
+  void* cnt[64] = {};
 };
 StaticScratch g_static_scratch;
 
@@ -855,23 +866,27 @@ extern "C" spectra_status spectra_decode_attend_noalloc(const spectra_codec* c, 
   int dev = 0;
   CUDA_TRY(cudaGetDevice(&dev));
   if (dev < 0 || dev >= 64) return fail(SPECTRA_ERR_UNSUPPORTED, "device ordinal above 63");
-  void* scratch = nullptr;
+  void *scratch = nullptr, *counters = nullptr;
   {
-    // First call on this device: look up the device address of the static array
-    // (the host-side symbol is not a device address).
+    // First call on this device: look up the device addresses of the static arrays
+    // (the host-side symbols are not device addresses).
     std::lock_guard<std::mutex> lock(g_static_scratch.mu);
     if (!g_static_scratch.ptr[dev]) {
-      void* p = nullptr;
+      void *p = nullptr, *n = nullptr;
       CUDA_TRY(cudaGetSymbolAddress(&p, g_static_decode_scratch));
+      CUDA_TRY(cudaGetSymbolAddress(&n, g_static_decode_counters));
+      g_static_scratch.cnt[dev] = n;
       g_static_scratch.ptr[dev] = p;
     }
     scratch = g_static_scratch.ptr[dev];
+    counters = g_static_scratch.cnt[dev];
   }
   const DecodePlan plan = make_decode_plan(c->h, cache->batch, cache->max_pages_per_seq);
-  if (plan.ws_bytes > kStaticScratchBytes)
-    return fail(SPECTRA_ERR_CAPACITY, "decode needs " + std::to_string(plan.ws_bytes) +
+  if (plan.rec_bytes > kStaticScratchBytes || (size_t)cache->batch * c->h.n_kv > kStaticCounters)
+    return fail(SPECTRA_ERR_CAPACITY, "decode needs " + std::to_string(plan.rec_bytes) +
                                           " bytes of scratch; the static area holds 4 MiB (use "
                                           "spectra_decode_attend with a caller workspace)");
-  CUDA_TRY(launch_decode(c->h, c->d, *cache, q, out, scratch, plan, static_cast<cudaStream_t>(stream)));
+  CUDA_TRY(launch_decode(c->h, c->d, *cache, q, out, static_cast<int32_t*>(counters), static_cast<float*>(scratch), plan,
+                         static_cast<cudaStream_t>(stream)));
   return SPECTRA_OK;
 }

@@ -195,15 +195,7 @@ DecodePlan make_decode_plan(const CodecDev& h, int batch, int max_pages_per_seq)
     }
   }
   p.n_split = best_ns;
-  size_t off = 0;
-  auto carve = [&](size_t bytes) {
-    const size_t o = off;
-    off += (bytes + 255) / 256 * 256;
-    return o;
-  };
-  p.cnt_off = carve((size_t)batch * h.n_kv * 4);
-  p.rec_off = carve((size_t)batch * h.n_kv * p.n_split * h.gq * p.rec_stride * 4);
-  p.ws_bytes = off;
+  p.rec_bytes = (size_t)batch * h.n_kv * p.n_split * h.gq * p.rec_stride * 4;
   std::lock_guard<std::mutex> lock(mu);
   memo[key] = p;
   return p;
@@ -309,10 +301,8 @@ cudaError_t launch_attend(const CodecDev& h, const CodecDev* d, const spectra_ca
 }  // namespace
 
 cudaError_t launch_decode(const CodecDev& h, const CodecDev* d, const spectra_cache& cache, const float* q,
-                          float* out, void* ws, const DecodePlan& plan, cudaStream_t st) {
-  uint8_t* w = static_cast<uint8_t*>(ws);
-  return launch_attend(h, d, cache, q, false, out, reinterpret_cast<float*>(w + plan.rec_off),
-                       reinterpret_cast<int32_t*>(w + plan.cnt_off), 0, plan.n_split, plan, st);
+                          float* out, int32_t* cnt, float* rec, const DecodePlan& plan, cudaStream_t st) {
+  return launch_attend(h, d, cache, q, false, out, rec, cnt, 0, plan.n_split, plan, st);
 }
 
 // Plan of a shared-prefix decode step; like the decode plan it depends on the
@@ -330,17 +320,13 @@ SharedPlan make_shared_plan(const CodecDev& h, int batch) {
   p.smem_bytes = prefix_smem_bytes(h, p.n_cols, &p.stages);
   const int slots = sm_count() * prefix_ctas_per_sm(p.n_cols, p.smem_bytes);
   p.n_prefix_split = std::max(1, std::min(kMaxSplit - p.own.n_split, slots / (h.n_kv * p.n_blocks)));
-  p.cnt_off = 0;
-  p.rec_off = ((size_t)batch * h.n_kv * 4 + 255) / 256 * 256;
-  p.ws_bytes = p.rec_off + (size_t)batch * h.n_kv * (p.own.n_split + p.n_prefix_split) * h.gq * p.own.rec_stride * 4;
+  p.rec_bytes = (size_t)batch * h.n_kv * (p.own.n_split + p.n_prefix_split) * h.gq * p.own.rec_stride * 4;
   return p;
 }
 
 cudaError_t launch_decode_shared(const CodecDev& h, const CodecDev* d, const spectra_cache& cache,
                                  const uint16_t* q, const int32_t* prefix_pages, int n_prefix, uint16_t* out,
-                                 void* ws, const SharedPlan& plan, cudaStream_t st) {
-  uint8_t* w = static_cast<uint8_t*>(ws);
-  float* rec = reinterpret_cast<float*>(w + plan.rec_off);
+                                 int32_t* cnt, float* rec, const SharedPlan& plan, cudaStream_t st) {
   int n_merge = plan.own.n_split;
   if (n_prefix > 0) {
     n_merge += plan.n_prefix_split;
@@ -348,8 +334,7 @@ cudaError_t launch_decode_shared(const CodecDev& h, const CodecDev* d, const spe
                                         plan.own.n_split, n_merge, plan, st);
     if (e != cudaSuccess) return e;
   }
-  return launch_attend(h, d, cache, q, true, out, rec, reinterpret_cast<int32_t*>(w + plan.cnt_off), n_prefix,
-                       n_merge, plan.own, st);
+  return launch_attend(h, d, cache, q, true, out, rec, cnt, n_prefix, n_merge, plan.own, st);
 }
 
 namespace attend {

@@ -142,13 +142,16 @@ struct DecodePlan {
   int off_stages;    // shared-memory offset of the ring
   int smem_bytes;    // dynamic shared memory per CTA
   int rec_stride;    // floats per cluster record of one q head
-  size_t cnt_off, rec_off, ws_bytes;  // workspace: arrival counters (zero between calls), split records
+  size_t rec_bytes;  // split records
 };
 DecodePlan make_decode_plan(const CodecDev& h, int batch, int max_pages_per_seq);
+constexpr int kDecodeMaxBatch = 65535;  // (a grid dimension)
+// A decode workspace begins with the arrival counters of the largest batch (zero between
+// calls), so that no batch's records reach another one's counters; the records follow.
+inline size_t decode_counter_bytes(const CodecDev& h) { return (size_t)(kDecodeMaxBatch + 1) * h.n_kv * 4; }
 cudaError_t launch_decode(const CodecDev& h, const CodecDev* d, const spectra_cache& cache,
-                          const float* q, float* out, void* ws, const DecodePlan& plan,
+                          const float* q, float* out, int32_t* cnt, float* rec, const DecodePlan& plan,
                           cudaStream_t st);
-constexpr int kSharedMaxBatch = 65535;  // (a grid dimension)
 // Decode over a shared prefix: the prefix kernel's records of every (sequence, q
 // head), then the decode kernel over the later pages, which merges both.
 struct SharedPlan {
@@ -158,12 +161,12 @@ struct SharedPlan {
   int n_blocks;      // blocks of query rows per KV head
   int stages;        // page stages of the prefix kernel's ring
   int smem_bytes;    // dynamic shared memory of the prefix kernel
-  size_t cnt_off, rec_off, ws_bytes;
+  size_t rec_bytes;  // records of both kernels
 };
 SharedPlan make_shared_plan(const CodecDev& h, int batch);
 cudaError_t launch_decode_shared(const CodecDev& h, const CodecDev* d, const spectra_cache& cache,
                                  const uint16_t* q, const int32_t* prefix_pages, int n_prefix, uint16_t* out,
-                                 void* ws, const SharedPlan& plan, cudaStream_t st);
+                                 int32_t* cnt, float* rec, const SharedPlan& plan, cudaStream_t st);
 
 // prefix_kernels.cu
 int prefix_columns(int rows);  // query rows of a prefix block for `rows` rows per KV head
