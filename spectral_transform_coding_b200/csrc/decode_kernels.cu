@@ -315,7 +315,7 @@ SharedPlan make_shared_plan(const CodecDev& h, int batch) {
   p.own = make_decode_plan(h, batch, 1 << 30);
   p.own.n_split = std::min(p.own.n_split, kMaxSplit / 2);
   const int rows = batch * h.gq;
-  p.n_cols = prefix_columns(rows);
+  p.n_cols = prefix_columns(h, rows);
   p.n_blocks = (rows + p.n_cols - 1) / p.n_cols;
   p.smem_bytes = prefix_smem_bytes(h, p.n_cols, &p.stages);
   const int slots = sm_count() * prefix_ctas_per_sm(p.n_cols, p.smem_bytes);

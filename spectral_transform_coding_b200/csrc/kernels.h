@@ -169,7 +169,7 @@ cudaError_t launch_decode_shared(const CodecDev& h, const CodecDev* d, const spe
                                  int32_t* cnt, float* rec, const SharedPlan& plan, cudaStream_t st);
 
 // prefix_kernels.cu
-int prefix_columns(int rows);  // query rows of a prefix block for `rows` rows per KV head
+int prefix_columns(const CodecDev& h, int rows);  // query rows of a prefix block for `rows` rows per KV head
 int prefix_smem_bytes(const CodecDev& h, int n_cols, int* stages);
 int prefix_ctas_per_sm(int n_cols, int smem);
 cudaError_t launch_prefix(const CodecDev& h, const CodecDev* d, const spectra_cache& cache, const uint16_t* q,

@@ -9,7 +9,7 @@
 //
 // Every code is unpacked once for up to 128 rows, so the work is that of two matrix
 // products and one exponential per (token, row):
-//   S^T [128 tokens x rows] = C_K [tokens x coordinates] Q^T,
+//   S^T [128 tokens x rows] = C_K [tokens x coordinates] Q^T (twice, for Q's two parts),
 //   O^T [coordinates x rows] += C_V^T [coordinates x tokens] P.
 // Both run on tcgen05 with fp32 accumulators in TMEM.  Tokens are S^T's TMEM lanes, so
 // the number of rows (the MMA's N) can be small without idle lanes; a thread holds one
@@ -18,8 +18,12 @@
 // Tiles of 128 tokens (8 blocks of 16, one or two warps each).  Per tile:
 //   1. unpack: a lane's 8 codes of a (block, group) come as fp16 integers by one
 //      and/or (code | 0x6400 = 1024 + code, or code << 4 | 0x5400 = 64 + code), one
-//      subtraction and one fma with the token's scale and zero: c = rn(code s + z),
-//      rounded once.  The packed layout is that of MMA fragments, so four lanes hold 8
+//      subtraction and one product with the token's scale.  Values: c = rn(code s + z),
+//      one fma, rounded once.  Keys exactly, as decode_attend's: c = (code - 2) s + 2 s + z,
+//      where (code - 2) s is an fp16 number for widths 1 and 2 (-2 s .. s) and the sum of two
+//      for the others (the second ones are further coordinates of the row), and 2 s and z of
+//      each group are two more coordinates, against the sum of the group's q_lat.
+//      The packed layout is that of MMA fragments, so four lanes hold 8
 //      adjacent coordinates of a token (K) or 8 adjacent tokens of a coordinate (V) and
 //      a warp's store fills whole 128-byte core matrices without bank conflicts.  K
 //      rows are ordered so that even tokens 2i and odd tokens 2i + 1 of a block's
@@ -44,10 +48,12 @@
 // 4x 96 us.  Of a tile's time the unpacking has about 43 %, the scores' way from TMEM over
 // exp2 to P 40 %.
 //
-// Rounding: q_lat, c and p to fp16 (2^-11 each); the product with fp16 pays 2^-11 of
-// |q_lat c| per coordinate in a score, well under the cache's own quantisation (a
-// code step is at least 2^-8 of a group's span).  The fold q W_up^K^T splits W_up into
-// two bf16 parts (2^-16).
+// Rounding: q_lat as two fp16 parts (2^-22), which multiply the exact keys, so that a score is
+// off by 2^-22 of its |q_lat c| and by the fold's two bf16 parts of W_up (2^-16).  (With one
+// part of q_lat and c = rn(code s + z) scores were off by 2^-11 of |q_lat| |c|: for keys far from
+// zero more than a code step, shared and own tokens' scores apart by it, outputs by up to six
+// times 2e-3; that took 3 to 12 us less a call.)  p is rounded to 2^-11 of itself, c_V to 2^-11 of
+// |c_V|: both average out over the tokens, and p's is also the decode kernel's.
 //
 // Every wait on an mbarrier is bounded; on a timeout the compute warps record
 // SPECTRA_ERR_TIMEOUT, agree in a vote, tell the MMA warp and leave; it waits for the
@@ -77,14 +83,17 @@ constexpr float kPfLimit = 15.9f;   // exponent of p above which m is taken agai
 
 // shared memory (bytes): barriers, tables, then V | K | Q | P | page ring
 constexpr int kPfBars = 0;       // uint64 [kPfMaxStages + 4]: pages, S, O, drain, fold
-constexpr int kPfMisc = 320;     // int: TMEM address, stop flag, pages of this CTA
+constexpr int kPfMisc = 320;     // int: TMEM address, stop flag, pages of this CTA, K steps and positions with low parts
 constexpr int kPfOrd = 384;      // int4 [2][kMaxG] groups in width-class order {block off, record off, group, width}
 constexpr int kPfOffs = 640;      // float [4][128] kPfOff - m of each row (added to a score), a copy per token quarter
 constexpr int kPfFac = 2688;      // float [4][128] the factors of a rescaling
 constexpr int kPfWMax = 4736;     // float [4][128] maxima, then sums, by token quarter
 constexpr int kPfOver = 6784;     // int [2][128] maxima above the limit, ordered as integers
 constexpr int kPfLane = 7808;     // uint4 [2][kMaxG][32] lane tables of the groups (width 8: not read)
-constexpr int kPfV = kPfLane + 2 * kMaxG * 512;  // operands (128-byte aligned)
+constexpr int kPfPos = kPfLane + 2 * kMaxG * 512;  // K groups: int [8] record offsets by position, int [8] bytes to the
+                                                   // low parts' chunks in class order, int [8] the steps of 16
+                                                   // coordinates with low parts
+constexpr int kPfV = kPfPos + 128;  // operands (128-byte aligned)
 static_assert(kPfV % 128 == 0, "core matrices are 128-byte blocks");
 
 // named barriers (0 is __syncthreads): the compute warps' vote; keys unpacked; P and
@@ -107,12 +116,16 @@ struct PrefixArgs {
   int n_q, n_kv, d_h, P, gq;
   int drop_page;  // test hook: page of CTA (0, 0, 0) whose copy is never issued; -1: none
   float q_scale;
-  alignas(16) int32_t hm[kMaxKV][8];  // as AttendArgs::hm
+  alignas(16) int32_t hm[kMaxKV][12];  // as AttendArgs::hm, then the chunks of a K row
 };
 
-// Bytes of K's (and Q's) coordinates per token row, in 16-byte chunks of 8: whole
-// MMA steps of 16, at least one.
-__host__ __device__ inline int k_chunks(int kept) { return kept > 0 ? (kept + 15) / 16 * 2 : 2; }
+// 16-byte chunks of 8 coordinates of a K row, whole MMA steps of 16:
+//   [kept coordinates, at least a step] [z of 8 groups | 2 s of 8 groups] [low parts of wide groups]
+// and of a Q row: [q_lat's high parts | its groups' sums twice] [low parts of both].
+__host__ __device__ inline int main_chunks(int kept) { return kept > 0 ? (kept + 15) / 16 * 2 : 2; }
+__host__ __device__ inline int q_chunks(int kept) { return 2 * (main_chunks(kept) + 2); }
+// Widths whose (code - 2) s has more bits than fp16 (width 2: -2 s .. s).
+__host__ __device__ inline bool wide_code(int b) { return b >= 3; }
 
 __device__ __forceinline__ void st_s32(uint32_t a, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
@@ -121,8 +134,8 @@ __device__ __forceinline__ void st_s128(uint32_t a, uint32_t x, uint32_t y, uint
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// The lane's 8-bit codes of one block (half `odd` of a 32-token block for G = 8) as four
-// registers of two fp16 integers each, fragment order (registers 1 and 3: rows + 8).
+// The lane's 8-bit codes (K side: less 2) of one block (half `odd` of a 32-token block for G = 8) as
+// four registers of two fp16 integers each, fragment order (registers 1 and 3: rows + 8).
 template <int G>
 __device__ __forceinline__ void load_bytes(uint32_t blk, int side, int odd, __half2 (&c)[4]) {
   uint32_t r[4];
@@ -144,7 +157,7 @@ __device__ __forceinline__ void load_bytes(uint32_t blk, int side, int odd, __ha
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     r[i] = (r[i] & 0x00FF00FFu) | 0x64006400u;
-    c[i] = __hsub2(*reinterpret_cast<__half2*>(&r[i]), __float2half2_rn(1024.f));
+    c[i] = __hsub2(*reinterpret_cast<__half2*>(&r[i]), __float2half2_rn(side == 0 ? 1026.f : 1024.f));
   }
 }
 
@@ -153,19 +166,23 @@ __device__ __forceinline__ uint32_t fma_bits(__half2 a, __half2 b, __half2 c) {
   const __half2 r = __hfma2(a, b, c);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+__device__ __forceinline__ uint32_t bits_of(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+// What rn(c s) lacks of c s; fp16 holds it exactly.
+__device__ __forceinline__ uint32_t low_part(__half2 c, __half2 s) { return fma_bits(c, s, __hneg2(__hmul2(c, s))); }
 
 __device__ __forceinline__ uint32_t ld_s32(uint32_t a) { return attend::ld_s32<0>(a); }
 __device__ __forceinline__ uint2 ld_s64(uint32_t a) { return attend::ld_s64<0>(a); }
 __device__ __forceinline__ uint4 ld_s128(uint32_t a) { return attend::ld_s128<0>(a); }
 
-// Maximum (or sum) over a warp's lanes of v[0..N): lane l ends with that of column
-// l / (32 / N) in v[0].  The lanes halve the columns they hold at each step.
-template <int N, bool MAX>
+// Maximum (or sum) over groups of L lanes of v[0..N): lane l of a group ends with that of column
+// l / (L / N) in v[0] (N > L: of N / L columns from l N / L on).  The lanes halve the columns they
+// hold at each step.
+template <int N, bool MAX, int L = 32>
 __device__ __forceinline__ void column_reduce(float (&v)[N], int lane) {
   auto op = [](float x, float y) { return MAX ? fmaxf(x, y) : x + y; };
   int w = N;
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
+  for (int o = L / 2; o >= 1; o >>= 1) {
     if (w > 1) {
       w >>= 1;
       const bool up = lane & o;
@@ -180,6 +197,13 @@ __device__ __forceinline__ void column_reduce(float (&v)[N], int lane) {
       v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
     }
   }
+}
+
+// x as two fp16 parts, the low one `low` bytes behind the high one.
+__device__ __forceinline__ void st_two_parts(uint32_t at, uint32_t low, float x) {
+  const __half hi = __float2half_rn(x), lo = __float2half_rn(x - __half2float(hi));
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(__half_as_ushort(hi)) : "memory");
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + low), "h"(__half_as_ushort(lo)) : "memory");
 }
 
 // (a0, a1) += (b0, b1) in one instruction; the largest of three in one.
@@ -239,13 +263,14 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, lon
 
 // Groups c .. c + U - 1 (past n_end: that one again, the same bytes to the same place) of a
 // block, all of width 4, 2 or 1, or all of width 3 (B3), from the lane table
-// `tab`: the loads of all of them first, then c = rn(code s + z) and the
-// stores.  K side (SIDE 0): coordinates 2 t4 (+ 8) of an even token (dst) and an odd one
-// (dst2); V side: coordinates gid (+ 8) of token pairs t4 and t4 + 4.
+// `tab`: the loads of all of them first, then the arithmetic and the stores.
+// K side (SIDE 0): (code - 2) s of coordinates 2 t4 (+ 8) of an even token (dst) and an odd
+// one (dst2), of the groups before n_lo in two parts, the low ones at their groups' offsets
+// `lo`; V side: c = rn(code s + z) of coordinates gid (+ 8) of token pairs t4 and t4 + 4.
 template <int G, int SIDE, int U, bool B3>
 __device__ __forceinline__ void unpack_batch(uint32_t tab, int c, int n_end, uint32_t sec, uint32_t blk, uint32_t rec,
                                              int tpp, uint32_t more_shift, uint32_t hi_word, uint32_t rot,
-                                             uint32_t dst, uint32_t dst2) {
+                                             int n_lo, uint32_t lo, uint32_t dst, uint32_t dst2) {
   uint4 d[U];  // {word offset, record offset, mask, shift | 32 width << 8 | operand offset << 16}
   uint32_t w[U], w3[U];
   uint2 ra[U], rb[U];
@@ -256,10 +281,11 @@ __device__ __forceinline__ void unpack_batch(uint32_t tab, int c, int n_end, uin
     const uint32_t code = sec + d[u].x + blk * __byte_perm(d[u].w, 0u, 0x4441);
     w[u] = ld_s32(code);
     if (B3) w3[u] = ld_s32(code + hi_word);  // code bit 2
-    ra[u] = ld_s64(sec + d[u].y + rec);
+    if (SIDE == 0) ra[u].x = ld_s32(sec + d[u].y + rec);
+    if (SIDE == 1) ra[u] = ld_s64(sec + d[u].y + rec);
     if (SIDE == 1) rb[u] = ld_s64(sec + d[u].y + rec + (uint32_t)(32 * tpp));
   }
-  const __half2 h1024 = __float2half2_rn(1024.f), h64 = __float2half2_rn(64.f);
+  const __half2 h1024 = __float2half2_rn(SIDE == 0 ? 1026.f : 1024.f), h64 = __float2half2_rn(SIDE == 0 ? 66.f : 64.f);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     {
@@ -273,12 +299,22 @@ __device__ __forceinline__ void unpack_batch(uint32_t tab, int c, int n_end, uin
       const __half2 c3 = __hsub2(as_half2((y & m4) | 0x54005400u), h64);
       const uint32_t o = d[u].w >> 16;
       if (SIDE == 0) {
-        const __half2 s = as_half2(ra[u].x), z = as_half2(ra[u].y);
-        st_s32(dst + o, fma_bits(c0, __low2half2(s), __low2half2(z)));
-        st_s32(dst2 + o, fma_bits(c1, __high2half2(s), __high2half2(z)));
+        const __half2 s = as_half2(ra[u].x), se = __low2half2(s), so = __high2half2(s);
+        st_s32(dst + o, bits_of(__hmul2(c0, se)));
+        st_s32(dst2 + o, bits_of(__hmul2(c1, so)));
         if (G == 16) {
-          st_s32(dst + o + 128, fma_bits(c2, __low2half2(s), __low2half2(z)));
-          st_s32(dst2 + o + 128, fma_bits(c3, __high2half2(s), __high2half2(z)));
+          st_s32(dst + o + 128, bits_of(__hmul2(c2, se)));
+          st_s32(dst2 + o + 128, bits_of(__hmul2(c3, so)));
+        }
+        const int k = min(c + u, n_end);
+        if (B3 || k < n_lo) {
+          const uint32_t l = ld_s32(lo + (uint32_t)k * 4u);
+          st_s32(dst + l, low_part(c0, se));
+          st_s32(dst2 + l, low_part(c1, so));
+          if (G == 16) {
+            st_s32(dst + l + 128, low_part(c2, se));
+            st_s32(dst2 + l + 128, low_part(c3, so));
+          }
         }
       } else {
         st_s32(dst + o, fma_bits(c0, as_half2(ra[u].x), as_half2(ra[u].y)));
@@ -293,11 +329,12 @@ __device__ __forceinline__ void unpack_batch(uint32_t tab, int c, int n_end, uin
 }
 
 // The kept groups of one side of a 16-token block (`blk16` of the page's section), all
-// of them or half `part` (pairs of the plain ones in turn, the others in turn).
+// of them or half `part` (pairs of the plain ones in turn, the others in turn).  K side:
+// groups of width 4 (the first n_four), 3 and 8 go in two parts.
 template <int G, int SIDE, int PARTS>
-__device__ __forceinline__ void unpack_block(const int4* ord, uint32_t tab, int n_plain, int n_three, int n_all, uint32_t sec,
-                                             int blk16, int tpp, int part, const LaneAddr& L, int gid, int t4,
-                                             uint32_t dst, uint32_t dst2) {
+__device__ __forceinline__ void unpack_block(const int4* ord, uint32_t tab, int n_four, int n_plain, int n_three, int n_all,
+                                             uint32_t sec, int blk16, int tpp, int part, const LaneAddr& L, int gid, int t4,
+                                             uint32_t lo, uint32_t dst, uint32_t dst2) {
   const uint32_t blk = (uint32_t)(G == 16 ? blk16 : blk16 >> 1), rec = (uint32_t)(blk16 * 8);
   const uint32_t more = G == 16 ? 0u : (uint32_t)((blk16 & 1) * (SIDE == 0 ? 8 : 4));
   constexpr int kAny = 1 << 20;  // no clamp
@@ -305,21 +342,21 @@ __device__ __forceinline__ void unpack_block(const int4* ord, uint32_t tab, int 
   for (int c = PARTS == 2 ? 2 * part : 0; c < n_plain; c += 4) {
     const int n = n_plain - c;
     if (PARTS == 2) {
-      unpack_batch<G, SIDE, 2, false>(tab, c, n_plain - 1, sec, blk, rec, tpp, more, 0u, 0u, dst, dst2);
+      unpack_batch<G, SIDE, 2, false>(tab, c, n_plain - 1, sec, blk, rec, tpp, more, 0u, 0u, n_four, lo, dst, dst2);
     } else if (n >= 4) {
-      unpack_batch<G, SIDE, 4, false>(tab, c, kAny, sec, blk, rec, tpp, more, 0u, 0u, dst, dst2);
+      unpack_batch<G, SIDE, 4, false>(tab, c, kAny, sec, blk, rec, tpp, more, 0u, 0u, n_four, lo, dst, dst2);
     } else {
-      if (n >= 2) unpack_batch<G, SIDE, 2, false>(tab, c, kAny, sec, blk, rec, tpp, more, 0u, 0u, dst, dst2);
-      if (n & 1) unpack_batch<G, SIDE, 1, false>(tab, c + n - 1, kAny, sec, blk, rec, tpp, more, 0u, 0u, dst, dst2);
+      if (n >= 2) unpack_batch<G, SIDE, 2, false>(tab, c, kAny, sec, blk, rec, tpp, more, 0u, 0u, n_four, lo, dst, dst2);
+      if (n & 1) unpack_batch<G, SIDE, 1, false>(tab, c + n - 1, kAny, sec, blk, rec, tpp, more, 0u, 0u, n_four, lo, dst, dst2);
     }
   }
 #pragma unroll 1
   for (int c = n_plain + (PARTS == 2 ? 2 * part : 0); c < n_three; c += 2 * PARTS) {
     const uint32_t hi = 64u + L.off1 - L.off2;
     if (PARTS == 2 || n_three - c >= 2)
-      unpack_batch<G, SIDE, 2, true>(tab, c, PARTS == 2 ? n_three - 1 : kAny, sec, blk, rec, tpp, more, hi, L.rot1, dst, dst2);
+      unpack_batch<G, SIDE, 2, true>(tab, c, PARTS == 2 ? n_three - 1 : kAny, sec, blk, rec, tpp, more, hi, L.rot1, n_four, lo, dst, dst2);
     else
-      unpack_batch<G, SIDE, 1, true>(tab, c, kAny, sec, blk, rec, tpp, more, hi, L.rot1, dst, dst2);
+      unpack_batch<G, SIDE, 1, true>(tab, c, kAny, sec, blk, rec, tpp, more, hi, L.rot1, n_four, lo, dst, dst2);
   }
 #pragma unroll 1
   for (int c = n_three + (PARTS == 2 ? part : 0); c < n_all; c += PARTS) {  // width 8
@@ -328,13 +365,13 @@ __device__ __forceinline__ void unpack_block(const int4* ord, uint32_t tab, int 
     load_bytes<G>(sec + (uint32_t)g.x + blk * 256u + L.off8, SIDE, blk16 & 1, v);
     const uint2 a = ld_s64(sec + (uint32_t)g.y + (uint32_t)((SIDE == 0 ? gid : t4) * tpp * 8) + rec);
     if (SIDE == 0) {
-      const __half2 s = as_half2(a.x), z = as_half2(a.y);
-      const uint32_t o = (uint32_t)(g.z * (G / 8 * 128));
-      st_s32(dst + o, fma_bits(v[0], __low2half2(s), __low2half2(z)));
-      st_s32(dst2 + o, fma_bits(v[1], __high2half2(s), __high2half2(z)));
-      if (G == 16) {
-        st_s32(dst + o + 128, fma_bits(v[2], __low2half2(s), __low2half2(z)));
-        st_s32(dst2 + o + 128, fma_bits(v[3], __high2half2(s), __high2half2(z)));
+      const __half2 s = as_half2(a.x), se = __low2half2(s), so = __high2half2(s);
+      const uint32_t o = (uint32_t)(g.z * (G / 8 * 128)), l = ld_s32(lo + (uint32_t)c * 4u);
+#pragma unroll
+      for (int i = 0; i < (G == 16 ? 4 : 2); ++i) {
+        const uint32_t at = (i & 1 ? dst2 : dst) + (uint32_t)(i / 2 * 128);
+        st_s32(at + o, bits_of(__hmul2(v[i], i & 1 ? so : se)));
+        st_s32(at + l, low_part(v[i], i & 1 ? so : se));
       }
     } else {
       const uint2 b = ld_s64(sec + (uint32_t)g.y + (uint32_t)((t4 + 4) * tpp * 8) + rec);
@@ -349,12 +386,36 @@ __device__ __forceinline__ void unpack_block(const int4* ord, uint32_t tab, int 
   }
 }
 
+// z and 2 s of every K group of a 16-token block: lane (pair of groups lane >> 3, pair of
+// tokens lane & 7); zeros for the groups that there are not.  dst: the z chunk's row of the even
+// token, dst2: of the odd one.
+__device__ __forceinline__ void unpack_offsets(uint32_t pos, int n_groups, uint32_t sec, int blk16, int tpp, int lane,
+                                               uint32_t dst, uint32_t dst2) {
+  const int p = (lane >> 3) * 2;
+  const uint32_t at = sec + (uint32_t)(((lane & 7) * tpp + blk16) * 8);
+  const uint2 off = ld_s64(pos + (uint32_t)p * 4u);
+  uint2 a = make_uint2(0u, 0u), b = a;
+  if (p < n_groups) a = ld_s64(at + off.x);
+  if (p + 1 < n_groups) b = ld_s64(at + off.y);
+  const uint32_t sa = bits_of(__hadd2(as_half2(a.x), as_half2(a.x))), sb = bits_of(__hadd2(as_half2(b.x), as_half2(b.x)));
+  const uint32_t word = (uint32_t)(lane >> 3) * 4u;
+  st_s32(dst + word, __byte_perm(a.y, b.y, 0x5410));
+  st_s32(dst2 + word, __byte_perm(a.y, b.y, 0x7632));
+  st_s32(dst + word + 128u, __byte_perm(sa, sb, 0x5410));
+  st_s32(dst2 + word + 128u, __byte_perm(sa, sb, 0x7632));
+}
+
 template <int G, int NB, int W, int CTAS>
 __global__ void __launch_bounds__(32 * W + 32, CTAS) prefix_kernel(const __grid_constant__ PrefixArgs A) {
   // W compute warps (8 or 16): 4 token quarters (TMEM lanes) x W / 4 parts of the rows for
   // the softmax; 8 blocks of a tile x W / 8 shares of the groups for the unpacking
   constexpr int kPfWarps = W, kPfCompute = 32 * W, kPfThreads = kPfCompute + 32, PARTS = W / 8;
   constexpr int HC = NB * 4 / W;         // rows (columns of S^T) per thread
+  // The next tile's keys are unpacked while this tile's scores wait in TMEM.  With 128 rows, whose
+  // operands leave the ring two tiles, they come after the scores have turned into P, when their
+  // pages have landed (64 x 28k at 4x: 171 us a call instead of 190; with fewer rows and a deep
+  // ring the later S would cost: 70.5 us instead of 69.2, 4 x 128k at 8x).
+  constexpr bool kLate = NB == 128;
   constexpr uint32_t kTmemCols = 4 * NB;  // (a power of two)
   constexpr uint32_t kS = 0, kO = 2 * NB;  // TMEM columns: two S buffers, O
   constexpr uint32_t kIdS = tc::idesc(kPfTok, NB, false), kIdO = tc::idesc(128, NB, true);
@@ -368,6 +429,7 @@ __global__ void __launch_bounds__(32 * W + 32, CTAS) prefix_kernel(const __grid_
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kPfMisc);
   volatile int* quit = reinterpret_cast<volatile int*>(smem + kPfMisc + 4);
   int* own_s = reinterpret_cast<int*>(smem + kPfMisc + 8);
+  int* low_s = reinterpret_cast<int*>(smem + kPfMisc + 12);  // K steps and positions (bits) with low parts
   int4* ord = reinterpret_cast<int4*>(smem + kPfOrd);
   float* wmax_s = reinterpret_cast<float*>(smem + kPfWMax);
   uint4* lane_t = reinterpret_cast<uint4*>(smem + kPfLane);
@@ -381,10 +443,11 @@ __global__ void __launch_bounds__(32 * W + 32, CTAS) prefix_kernel(const __grid_
   const int sub = warp & 3, col0 = ((warp >> 2) & (W / 4 - 1)) * HC;  // its TMEM lanes and rows
   const int block = warp & 7, part = PARTS == 2 ? (warp >> 3) & 1 : 0;  // its 16-token block of a tile, its share
   // (read once: the compiler reloads a dynamically indexed parameter after every asm)
-  const int4 hm0 = reinterpret_cast<const int4*>(A.hm[a])[0], hm1 = reinterpret_cast<const int4*>(A.hm[a])[1];
+  const int4 hm0 = reinterpret_cast<const int4*>(A.hm[a])[0], hm1 = reinterpret_cast<const int4*>(A.hm[a])[1],
+             hm2 = reinterpret_cast<const int4*>(A.hm[a])[2];
   const int sec_off = hm0.x, sec_bytes = hm0.y;
   const int P = A.P, tpp = P / 16, S = A.stages, nK = hm0.z, nV = hm0.w, nkK = hm1.x, nkV = hm1.y;
-  const int nkd = k_chunks(nkK);
+  const int nkd = main_chunks(nkK), ck = hm2.x, cq = q_chunks(nkK);  // chunks: kept coordinates, K row, Q row
   LaneAddr L;
   L.off4 = lane * 4;
   L.off8 = lane * 8;
@@ -397,7 +460,7 @@ __global__ void __launch_bounds__(32 * W + 32, CTAS) prefix_kernel(const __grid_
   // ---- tables ---------------------------------------------------------------------
   const DecodeOrder* __restrict__ dec = &cd->head[a].dec;
   // groups of width 4, 2 and 1 come first, then those of width 3
-  const int plainK = dec->cls[0][3], plainV = dec->cls[1][3], threeK = dec->cls[0][4], threeV = dec->cls[1][4];
+  const int fourK = dec->cls[0][1], plainK = dec->cls[0][3], plainV = dec->cls[1][3], threeK = dec->cls[0][4], threeV = dec->cls[1][4];
   if (warp < kPfWarps) {
 #pragma unroll
     for (int s = part; s < 2; s += PARTS) {  // this warp's entries of the sides' lists
@@ -409,6 +472,23 @@ __global__ void __launch_bounds__(32 * W + 32, CTAS) prefix_kernel(const __grid_
       lane_t[e * 32 + lane] =
           make_uint4((uint32_t)g.x + off, (uint32_t)(g.y + (s ? t4 : gid) * tpp * 8), ((1u << g.w) - 1u) * 0x00010001u,
                      sh | (uint32_t)(g.w << 13) | (uint32_t)(g.z * (s ? G / 8 * 2048 : G / 8 * 128)) << 16);
+    }
+  }
+  int* pos_s = reinterpret_cast<int*>(smem + kPfPos);  // [3][8], see kPfPos
+  if (warp == 0) {
+    const int4 g = lane < nK ? __ldg(reinterpret_cast<const int4*>(dec->ord[0][lane])) : make_int4(0, 0, 0, 0);
+    const int step = g.z * G / 16;
+    const bool wide = lane < nK && wide_code(g.w);
+    const uint32_t steps = __reduce_or_sync(0xffffffffu, wide ? 1u << step : 0u);
+    const uint32_t wides = __reduce_or_sync(0xffffffffu, wide ? 1u << g.z : 0u);
+    if (lane < nK) {
+      pos_s[g.z] = g.y;
+      pos_s[kMaxG + lane] = (nkd + 2 + 2 * __popc(steps & ((1u << step) - 1u)) + (G == 8 ? g.z & 1 : 0)) * 128;
+    }
+    if ((steps >> lane) & 1u) pos_s[2 * kMaxG + __popc(steps & ((1u << lane) - 1u))] = lane;
+    if (lane == 0) {
+      low_s[0] = (int)steps;
+      low_s[1] = (int)wides;
     }
   }
   // pages of at most 128 tokens: `pages_per` whole pages per tile; longer pages:
@@ -486,7 +566,8 @@ __global__ void __launch_bounds__(32 * W + 32, CTAS) prefix_kernel(const __grid_
         __syncwarp();
       }
     }
-    const uint64_t dK = tc::desc(sK, 128, nkd * 128), dQ = tc::desc(sQ, 128, nkd * 128);
+    const uint64_t dK = tc::desc(sK, 128, ck * 128), dQ = tc::desc(sQ, 128, cq * 128);
+    const int n_main = nkd / 2, n_low = __popc((uint32_t)low_s[0]);
     const uint64_t dV = tc::desc(sV, 128, 2048), dP = tc::desc(sP, 128, 2048);
     int t = -1;
     for (; t < T; ++t) {  // iteration t: S of tile t + 1, then O of tile t
@@ -495,8 +576,14 @@ __global__ void __launch_bounds__(32 * W + 32, CTAS) prefix_kernel(const __grid_
         tc::fence_after();
         if (tc::elect()) {
           const uint32_t d = tmem + kS + (uint32_t)(((t + 1) & 1) * NB);
-          for (int k = 0; k < nkd / 2; ++k)
+#pragma unroll 1
+          for (int k = 0; k <= n_main; ++k) {  // the last: z and 2 s
             tc::mma(d, dK + (uint64_t)(k * 16), dQ + (uint64_t)(k * 16), kIdS, k > 0);
+            tc::mma(d, dK + (uint64_t)(k * 16), dQ + (uint64_t)((n_main + 1 + k) * 16), kIdS, true);
+          }
+#pragma unroll 1
+          for (int i = 0; i < n_low; ++i)
+            tc::mma(d, dK + (uint64_t)((n_main + 1 + i) * 16), dQ + (uint64_t)(pos_s[2 * kMaxG + i] * 16), kIdS, true);
           tc::commit(bar_s);
         }
         __syncwarp();
@@ -614,23 +701,47 @@ __global__ void __launch_bounds__(32 * W + 32, CTAS) prefix_kernel(const __grid_
       float v[HC];
       tc::ld<HC>(lane_base + kS, v);
       tc::fence_before();
-      if (row < nkd * 8) {  // coordinate `row` (zero beyond the kept ones) of rows col0 ..
-        const uint32_t at = sQ + (uint32_t)((col0 / 8) * nkd * 128 + (row >> 3) * 128 + (row & 7) * 2 + (col0 & 7) * 16);
+      // coordinate `row` (zero beyond the kept ones) of rows col0 .., and its group's sum
+      const uint32_t low = (uint32_t)((nkd + 2) * 128);
+      const uint32_t at = sQ + (uint32_t)((col0 / 8) * cq * 128 + (row >> 3) * 128 + (row & 7) * 2 + (col0 & 7) * 16);
+      const int g = row / G;
+      const uint32_t at_sum = sQ + (uint32_t)((col0 / 8) * cq * 128 + nkd * 128 + g * 2 + (col0 & 7) * 16);
 #pragma unroll
-        for (int c = 0; c < HC; ++c) {
-          const unsigned short h = __half_as_ushort(__float2half_rn(v[c] * A.q_scale));
-          asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + (uint32_t)((c >> 3) * nkd * 128 + (c & 7) * 16)), "h"(h)
-                       : "memory");
+      for (int c = 0; c < HC; ++c) {
+        v[c] *= A.q_scale;
+        if (row < nkd * 8) st_two_parts(at + (uint32_t)((c >> 3) * cq * 128 + (c & 7) * 16), low, v[c]);
+      }
+      column_reduce<HC, false, G>(v, lane);
+      constexpr int kMine = HC > G ? HC / G : 1, kSame = HC > G ? 1 : G / HC;  // columns of a lane, lanes of a column
+      if (g < kMaxG && lane % kSame == 0) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int c = lane % G / kSame * kMine + i;
+          const uint32_t at_c = at_sum + (uint32_t)((c >> 3) * cq * 128 + (c & 7) * 16);
+          const float sum = g < nK ? v[i] : 0.f;
+          st_two_parts(at_c, low, sum);         // times z
+          st_two_parts(at_c + 128u, low, sum);  // times 2 s
         }
       }
     }
-    // the padding chunk of K (an odd number of 8-coordinate groups, or no keys at all)
-    for (int kd = nkK / 8; kd < nkd; ++kd)
-      if (tid < kPfTok) st_s128(sK + (uint32_t)(((tid >> 3) * nkd + kd) * 128 + (tid & 7) * 16), 0u, 0u, 0u, 0u);
+    // the chunks of K that no group writes: padding (an odd number of 8-coordinate groups, or no
+    // keys at all) and, beside the low parts of a group of 8, those of its step's other group
+    if (tid < kPfTok) {
+      const uint32_t at = sK + (uint32_t)((tid >> 3) * ck * 128 + (tid & 7) * 16);
+      for (int kd = nkK / 8; kd < nkd; ++kd) st_s128(at + (uint32_t)(kd * 128), 0u, 0u, 0u, 0u);
+      if (G == 8) {
+        const uint32_t steps = (uint32_t)low_s[0], wides = (uint32_t)low_s[1];
+        for (int p = 0; p < 2 * (nkd / 2); ++p)
+          if (((steps >> (p >> 1)) & 1u) && !((wides >> p) & 1u))
+            st_s128(at + (uint32_t)((nkd + 2 + 2 * __popc(steps & ((1u << (p >> 1)) - 1u)) + (p & 1)) * 128), 0u, 0u, 0u, 0u);
+      }
+    }
 
     // ---- tiles --------------------------------------------------------------------
     const uint32_t tabK = smem_u32(lane_t) + (uint32_t)(lane * 16), tabV = tabK + kMaxG * 512;
-    const uint32_t k_dst = sK + (uint32_t)((block * 2 + (gid >> 2)) * nkd * 128 + t4 * 4);
+    const uint32_t k_dst = sK + (uint32_t)((block * 2 + (gid >> 2)) * ck * 128 + t4 * 4);
+    const uint32_t z_dst = sK + (uint32_t)(((block * 2 + ((lane & 7) >> 2)) * ck + nkd) * 128);
+    const uint32_t pos_a = smem_u32(pos_s);
     const uint32_t v_dst = sV + (uint32_t)(block * 256 + gid * 16 + t4 * 4);
     // this warp's block of the tile whose keys come next: page (of this CTA's list) and
     // its stage and phase, first token in the page; the block whose values come next
@@ -646,8 +757,11 @@ __global__ void __launch_bounds__(32 * W + 32, CTAS) prefix_kernel(const __grid_
       if (here && (sec_bytes == 0 || wait(&bars[stage], phase))) {
         v_sec = sec;
         v_blk = tau >> 4;
-        unpack_block<G, 0, PARTS>(ord, tabK, plainK, threeK, nK, sec, v_blk, tpp, part, L, gid, t4, k_dst + (uint32_t)(gid * 16),
-                           k_dst + (uint32_t)((gid ^ 4) * 16));
+        unpack_block<G, 0, PARTS>(ord, tabK, fourK, plainK, threeK, nK, sec, v_blk, tpp, part, L, gid, t4, pos_a + 32u,
+                                  k_dst + (uint32_t)(gid * 16), k_dst + (uint32_t)((gid ^ 4) * 16));
+        if (part == PARTS - 1)
+          unpack_offsets(pos_a, nK, sec, v_blk, tpp, lane, z_dst + (uint32_t)((lane & 7) * 16),
+                         z_dst + (uint32_t)(((lane & 7) ^ 4) * 16));
       }
       int adv = pages_per;
       if (!small) {
@@ -660,6 +774,15 @@ __global__ void __launch_bounds__(32 * W + 32, CTAS) prefix_kernel(const __grid_
       if (stage >= S) {
         stage -= S;
         phase ^= 1;
+      }
+    };
+
+    auto next_keys = [&](int t) {
+      if (t + 1 < T) {
+        unpack_keys();
+        fence_proxy_async_smem();
+        tc::fence_before();
+        bar_arrive<kPfThreads>(kBarKeys);
       }
     };
 
@@ -684,12 +807,7 @@ __global__ void __launch_bounds__(32 * W + 32, CTAS) prefix_kernel(const __grid_
       tc::fence_after();
       const uint32_t sec_t = v_sec;
       const int blk_t = v_blk;
-      if (t + 1 < T) {
-        unpack_keys();
-        fence_proxy_async_smem();
-        tc::fence_before();
-        bar_arrive<kPfThreads>(kBarKeys);
-      }
+      if (!kLate) next_keys(t);
       // tokens of a short tile's missing blocks: none
       const int n_blk = small ? min(pages_per, n_own - t * pages_per) * tpp : min(kPfTok, P - sub_tile * kPfTok) / 16;
       if (!small && ++sub_tile == tiles_per) sub_tile = 0;
@@ -736,6 +854,7 @@ __global__ void __launch_bounds__(32 * W + 32, CTAS) prefix_kernel(const __grid_
         if (bar_vote<kPfCompute>(failed_now)) {
           done = false;
           *quit = 1;
+          if (kLate && t + 1 < T) bar_arrive<kPfThreads>(kBarKeys);  // (which the MMA warp waits for first)
           bar_arrive<kPfThreads>(kBarValues);  // (orders the flag before the MMA warp's look at it)
           break;
         }
@@ -801,8 +920,10 @@ __global__ void __launch_bounds__(32 * W + 32, CTAS) prefix_kernel(const __grid_
         for (int c = 0; c < HC / 8; ++c)
           st_s128(p_dst + c * 2048, pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
       }
+      if (kLate) next_keys(t);
       if (blk_t >= 0)
-        unpack_block<G, 1, PARTS>(ord + kMaxG, tabV, plainV, threeV, nV, sec_t, blk_t, tpp, part ^ (PARTS - 1), L, gid, t4, v_dst, 0u);
+        unpack_block<G, 1, PARTS>(ord + kMaxG, tabV, 0, plainV, threeV, nV, sec_t, blk_t, tpp, part ^ (PARTS - 1), L, gid, t4,
+                                  0u, v_dst, 0u);
       fence_proxy_async_smem();
       tc::fence_before();
       bar_arrive<kPfThreads>(kBarValues);
@@ -873,26 +994,41 @@ PrefixKernel prefix_kernel_of(int n_cols, int ctas, int* warps) {
   }
 }
 
+// Chunks of a K row of head `hd`: kept coordinates, z and 2 s, a step for each with a wide group.
+int k_chunks(const CodecDev& h, const HeadDev& hd) {
+  const SideDev& k = hd.side[0];
+  uint32_t steps = 0;
+  for (int j = 0; j < k.n_groups; ++j)
+    if (wide_code(k.grp[j].b)) steps |= 1u << (j * h.group / 16);
+  int n = 0;
+  for (; steps; steps &= steps - 1) ++n;
+  return main_chunks(k.n_kept) + 2 + 2 * n;
+}
+
 struct PrefixSmem {
   int off_k, off_q, off_p, off_ring, stage_bytes, stages, total, fold_dims;
 };
+
+constexpr int kPfSmemMax = 226 * 1024;  // of a CTA that has an SM for itself
 
 // V, K, Q, P, and as many page stages as leave room for two CTAs per SM, else for one: two tiles'
 // pages at least, eight tiles' at most.
 PrefixSmem prefix_smem(const CodecDev& h, int n_cols) {
   PrefixSmem s{};
   auto up = [](int x) { return (x + 127) / 128 * 128; };
-  const int nkd = k_chunks(h.max_kept_k);
+  const int nkd = main_chunks(h.max_kept_k);
+  int ck = 0;
+  for (int a = 0; a < h.n_kv; ++a) ck = std::max(ck, k_chunks(h, h.head[a]));
   s.off_k = up(kPfV + h.max_kept_v / 8 * 2048);
-  s.off_q = s.off_k + 16 * nkd * 128;
-  s.off_p = s.off_q + n_cols / 8 * nkd * 128;
+  s.off_q = s.off_k + 16 * ck * 128;
+  s.off_p = s.off_q + n_cols / 8 * q_chunks(h.max_kept_k) * 128;
   s.off_ring = s.off_p + n_cols / 8 * 2048;
   // the fold's W_up^K takes V's, K's and Q's bytes (its MMA reads 128 coordinates)
   s.fold_dims = h.d_h > 64 && nkd * 4096 <= s.off_p - kPfV ? 128 : 64;
   s.stage_bytes = std::max(16, (h.max_sec_bytes + 15) / 16 * 16);
   const int per = h.P <= kPfTok ? kPfTok / h.P : 1;
   const int lo = 2 * per, hi = std::min(kPfMaxStages, 8 * per);
-  const int one = 226 * 1024, two = 113 * 1024;
+  const int one = kPfSmemMax, two = 113 * 1024;
   auto fit = [&](int budget) { return std::min(hi, std::max(0, budget - s.off_ring) / s.stage_bytes); };
   s.stages = n_cols == 128 ? 0 : fit(two);
   if (s.stages < lo) s.stages = std::max(lo, fit(one));
@@ -906,7 +1042,13 @@ PrefixSmem prefix_smem(const CodecDev& h, int n_cols) {
 // The fewest columns of 16, 32, 64 and 128 that hold the rows (128: several blocks).
 // Fewer columns cost fewer score and exp2 instructions a token; in blocks of 64 rows 64
 // sequences x 28k at 4x unpacked every code four times and took 239 us, in blocks of 128 165 us.
-int prefix_columns(int rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)); }
+// Fewer where two tiles' pages would not fit beside the operands (many wide groups; 32 always fit:
+// 8 groups of 16 at 8 bits on both sides, the most there is, take 227,072 bytes).
+int prefix_columns(const CodecDev& h, int rows) {
+  int n = rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128));
+  while (n > 32 && prefix_smem(h, n).total > kPfSmemMax) n /= 2;
+  return n;
+}
 
 int prefix_smem_bytes(const CodecDev& h, int n_cols, int* stages) {
   const PrefixSmem s = prefix_smem(h, n_cols);
@@ -970,6 +1112,7 @@ cudaError_t launch_prefix(const CodecDev& h, const CodecDev* d, const spectra_ca
     m[5] = hd.side[1].n_kept;
     m[6] = hd.wupk_rows_off;
     m[7] = hd.side[1].wup_off;
+    m[8] = k_chunks(h, hd);
   }
   int warps = 0;
   const int ctas = prefix_ctas_per_sm(plan.n_cols, s.total);

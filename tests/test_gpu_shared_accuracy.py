@@ -1,0 +1,79 @@
+"""Decode attention over a shared prefix where its roundings count: keys far from zero; each output
+element against softmax attention in 64 bits over the dequantised latents.
+
+Bar: 2e-3 of the row's largest value, the decode attention's own, and half a step of bf16 (2^-8 of the value)."""
+import numpy as np
+import pytest
+
+from gpu_helpers import dev, kept_wup, synthetic_latents, torch_mod
+from test_gpu_shared_prefix import _codec, _queries, _sides
+
+pytestmark = pytest.mark.gpu
+
+
+def _with_latents(s, n_prefix, own, lat, seed):
+    """Cache whose sequences share the latents `lat` [n_prefix P][n_eff] and hold own[b] [n][n_eff] of their own."""
+    torch = torch_mod()
+    import spectral_transform_coding_b200 as st
+    codec, P, B = s["codec"], s["P"], len(own)
+    extra = max([1] + [-(-len(x) // P) for x in own])
+    ids = np.random.default_rng(seed).permutation(n_prefix + B * extra).astype(np.int32)
+    table = np.concatenate([np.tile(ids[:n_prefix], (B, 1)), ids[n_prefix:].reshape(B, extra)], 1)
+    cache = st.LatentCache(codec, batch=B, max_pages_per_seq=n_prefix + extra, n_pages=ids.size, device=dev(),
+                           page_table=torch.from_numpy(table))
+    codec.quantize_append(cache, torch.from_numpy(lat).to(dev()), torch.zeros(len(lat), dtype=torch.int32, device=dev()))
+    cache.lengths.fill_(n_prefix * P)
+    rows, seqs = np.concatenate(own), np.concatenate([np.full(len(x), b, np.int32) for b, x in enumerate(own)])
+    if len(rows):
+        codec.quantize_append(cache, torch.from_numpy(rows).to(dev()), torch.from_numpy(seqs).to(dev()))
+    codec.device_status()
+    return cache, table, torch.from_numpy(ids[:n_prefix]).to(dev()), cache.lengths.cpu().numpy()
+
+
+def _bar(s, cache, table, lengths, q, outs):
+    """Largest error of each of `outs` [batch][heads][d_head] in units of the bar."""
+    W = kept_wup(s["W_up"], s["widths"], s["group"])
+    gq = s["n_q"] // s["n_kv"]
+    s.pop("pool", None)
+    worst = np.zeros(len(outs))
+    for b in range(len(lengths)):
+        for a in range(s["n_kv"]):
+            (cK, _), (cV, _) = _sides(s, cache, table, lengths, b, a)
+            for h in range(a * gq, (a + 1) * gq):
+                sc = cK @ (np.asarray(W[a][0], np.float64) @ q[b, h]) / np.sqrt(s["d_h"])
+                w = np.exp(sc - sc.max())
+                ref = (w / w.sum() @ cV) @ np.asarray(W[a][1], np.float64)
+                bar = 2.0 ** -8 * np.abs(ref) + 2e-3 * np.abs(ref).max()
+                for i, out in enumerate(outs):
+                    off = np.abs(out[b, h] - ref) / bar
+                    worst[i] = max(worst[i], float(off.max()) if np.isfinite(off).all() else np.inf)
+    return worst
+
+
+@pytest.mark.parametrize("name", ["llama4x", "qwen8x", "g8wide", "allwidths"])
+def test_keys_far_from_zero(name):
+    """Keys with a common offset of many times their spread, as a projection with a bias gives them: the shared decode,
+    the same with fewer pages shared, and the decode that shares nothing are all within the bar."""
+    torch = torch_mod()
+    s = _codec(name, 31)
+    codec, P = s["codec"], s["P"]
+    n_prefix = -(-400 // P)
+    rng = np.random.default_rng(32)
+    off = rng.choice([-50.0, 50.0], codec.n_eff).astype(np.float32)
+    kept = kept_wup(s["W_up"], s["widths"], s["group"])
+    col = 0
+    for a in range(s["n_kv"]):  # (the value columns stay where they are)
+        col += len(kept[a][0])
+        off[col:col + len(kept[a][1])] = 0.0
+        col += len(kept[a][1])
+    assert col == codec.n_eff
+    make = lambda n, k: synthetic_latents(n, codec.n_eff, seed=33 + k, decay=0.2) + off  # noqa: E731
+    cache, table, prefix, lengths = _with_latents(s, n_prefix, [make(100, 1), make(0, 2)], make(n_prefix * P, 0), 34)
+    q, q64 = _queries(s, 2, 35, scale=1.0)
+    outs = [codec.decode_attend_shared(cache, q, prefix), codec.decode_attend_shared(cache, q, prefix[:n_prefix // 2]),
+            codec.decode_attend(cache, q.float())]
+    codec.device_status()
+    worst = _bar(s, cache, table, lengths, q64, [o.double().cpu().numpy() for o in outs])
+    assert worst[2] <= 1.0
+    assert worst[1] <= 1.0
+    assert worst[0] <= 1.0
