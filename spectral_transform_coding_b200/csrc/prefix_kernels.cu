@@ -2,7 +2,7 @@
 // latent cache (spectra_decode_attend_shared).
 //
 // For the rows r = (sequence, q head) of KV head a, with the latents c of the shared
-// pages:  s_rt = q_lat,r . c_K,t (log2 units),  m_r >= max_t s_rt - 18.9,
+// pages:  s_rt = q_lat,r . c_K,t (log2 units),  m_r >= max_t s_rt - 7.9,
 // l_r = sum_t 2^(s_rt - m_r),  o_r = sum_t 2^(s_rt - m_r) c_V,t.  Each CTA leaves
 // (m, l, o) of its part of the prefix in the records that the decode kernel merges
 // with those of the sequences' own pages.
@@ -28,10 +28,10 @@
 //      a warp's store fills whole 128-byte core matrices without bank conflicts.  K
 //      rows are ordered so that even tokens 2i and odd tokens 2i + 1 of a block's
 //      half take rows i and i ^ 4 of its core matrix;
-//   2. scores from TMEM; p = 2^(s - m - 3) as fp16, P in shared memory with the
+//   2. scores from TMEM; p = 2^(s - m + 8) as fp16, P in shared memory with the
 //      rows contiguous (each thread writes its token's line in 16-byte pieces).
 // m is not the running maximum but a maximum taken when a score last exceeded it by
-// more than 18 (p < 2^16 fits fp16); the check costs one max per score and one vote
+// more than 7.9 (p < 2^16 fits fp16); the check costs one max per score and one vote
 // that the tile's barrier carries, and the exact maxima and the rescaling of O run
 // only then (always in the first tile).  l is summed in fp32 registers per thread (as a
 // third product, of P with ones, it doubles the MMAs of the tile's second half: 16
@@ -78,7 +78,11 @@ using attend::LaneAddr;
 
 constexpr int kPfTok = 128;       // tokens of a tile
 constexpr int kPfMaxStages = 32;
-constexpr float kPfOff = -3.f;      // p = 2^(s - m - 3)
+// p = 2^(s - m + 8), as the decode kernel's: all 11 bits down to 2^-22 of a split's largest weight,
+// nothing lost above 2^-32.  (From 2^-3 instead of 2^8 the first tile's m served longer, and 16
+// sequences x 32k at 12x took 2 us less, but weights below 2^-22 of the largest vanished from O and
+// stayed in l: behind a first token with 0.99 of the weight and no value the output was several percent off.)
+constexpr float kPfOff = attend::kPScaleLog2;
 constexpr float kPfLimit = 15.9f;   // exponent of p above which m is taken again (fp16 ends at 2^15.999)
 
 // shared memory (bytes): barriers, tables, then V | K | Q | P | page ring

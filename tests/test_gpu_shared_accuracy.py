@@ -1,5 +1,5 @@
-"""Decode attention over a shared prefix where its roundings count: keys far from zero; each output
-element against softmax attention in 64 bits over the dequantised latents.
+"""Decode attention over a shared prefix where its roundings count: a first token that holds most of the weight and has
+no value, and keys far from zero; each output element against softmax attention in 64 bits over the dequantised latents.
 
 Bar: 2e-3 of the row's largest value, the decode attention's own, and half a step of bf16 (2^-8 of the value)."""
 import numpy as np
@@ -48,6 +48,33 @@ def _bar(s, cache, table, lengths, q, outs):
                     off = np.abs(out[b, h] - ref) / bar
                     worst[i] = max(worst[i], float(off.max()) if np.isfinite(off).all() else np.inf)
     return worst
+
+
+@pytest.mark.parametrize("batch", [1, 9])
+@pytest.mark.parametrize("nats", [13.0, 15.5, 17.0])
+def test_a_first_token_with_most_of_the_weight_and_no_value(nats, batch):
+    """28,672 shared tokens with scores of deviation about 1; the first token's is `nats`, so that it takes between 0.8
+    and 0.999 of the weight, and its value is zero: the output is what the other tokens' small weights leave."""
+    torch = torch_mod()
+    s = _codec("qwen8x", 21)
+    P, n_prefix = s["P"], 448
+    rng = np.random.default_rng(22)
+    lat = rng.standard_normal((n_prefix * P, s["codec"].n_eff)).astype(np.float32)
+    lat[:, 0] = 0.0
+    lat[0] = 0.0
+    W0 = np.asarray(kept_wup(s["W_up"], s["widths"], s["group"])[0][0][0], np.float64)  # K coordinate 0
+    g = rng.standard_normal((batch, s["n_q"], s["d_h"])) * 1.4
+    g += (8.0 - g @ W0)[..., None] * W0 / (W0 @ W0)
+    lat[0, 0] = nats * np.sqrt(s["d_h"]) / 8.0
+    q = torch.from_numpy(g.astype(np.float32)).to(dev()).to(torch.bfloat16)
+    cache, table, prefix, lengths = _with_latents(s, n_prefix, [lat[:0]] * batch, lat, 23)
+    out = s["codec"].decode_attend_shared(cache, q, prefix)
+    s["codec"].device_status()
+    (cK, _), (cV, _) = _sides(s, cache, table, lengths, 0, 0)
+    assert np.all(cV[0] == 0) and np.count_nonzero(cK[0]) == 1
+    rows = slice(0, 1) if batch == 1 else slice(0, 9, 8)
+    worst = _bar(s, cache, table[rows], lengths[rows], q.double().cpu().numpy()[rows], [out.double().cpu().numpy()[rows]])
+    assert worst[0] <= 1.0
 
 
 @pytest.mark.parametrize("name", ["llama4x", "qwen8x", "g8wide", "allwidths"])
