@@ -104,3 +104,21 @@ def test_keys_far_from_zero(name):
     assert worst[2] <= 1.0
     assert worst[1] <= 1.0
     assert worst[0] <= 1.0
+
+
+@pytest.mark.parametrize("own", [[0, 0], [0, 7], [70, 0]])
+def test_a_nan_query_gives_nan_with_and_without_own_tokens(own):
+    torch = torch_mod()
+    s = _codec("qwen8x", 41)
+    n_eff = s["codec"].n_eff
+    lat = synthetic_latents(4 * s["P"], n_eff, seed=42)
+    cache, _, prefix, _ = _with_latents(s, 4, [synthetic_latents(n, n_eff, seed=43 + n) for n in own], lat, 44)
+    q, _ = _queries(s, 2, 45)
+    want = s["codec"].decode_attend_shared(cache, q, prefix)
+    q[0, 2] = float("nan")
+    got = s["codec"].decode_attend_shared(cache, q, prefix)
+    s["codec"].device_status()
+    assert torch.isnan(got[0, 2]).all()
+    keep = torch.ones_like(got[:, :, 0], dtype=torch.bool)
+    keep[0, 2] = False
+    assert torch.equal(got[keep], want[keep])
