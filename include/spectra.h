@@ -469,7 +469,10 @@ SPECTRA_API void spectra_planner_destroy(spectra_planner* planner);
  * few or the total exceeds max_tokens (SPECTRA_ERR_CAPACITY), or if a length or
  * token count is negative, a length above 0 is below n_prefix * P or a sequence of
  * length 0 gets tokens although n_prefix > 0 (SPECTRA_ERR_INVALID), the planner's
- * error word is set and nothing is written.  batch <= 16384, max_tokens <= 2^24. */
+ * error word is set and nothing is written.  batch <= 16384, max_tokens <= 2^24.
+ * The array of free_pages must hold *n_free entries: spectra_plan_append_ex, the
+ * same with the array's size, checks that (SPECTRA_ERR_INVALID) before it reads
+ * an entry. */
 SPECTRA_API spectra_status spectra_plan_append(const spectra_planner* planner, int32_t batch,
                                                const int32_t* lengths, const int32_t* new_tokens,
                                                const int32_t* prefix_pages, int32_t n_prefix,
@@ -478,6 +481,14 @@ SPECTRA_API spectra_status spectra_plan_append(const spectra_planner* planner, i
                                                int32_t max_pages_per_seq, int64_t max_tokens, int32_t* seq_ids,
                                                int32_t* positions, int64_t* slots, int32_t* offsets,
                                                void* stream);
+SPECTRA_API spectra_status spectra_plan_append_ex(const spectra_planner* planner, int32_t batch,
+                                                  const int32_t* lengths, const int32_t* new_tokens,
+                                                  const int32_t* prefix_pages, int32_t n_prefix,
+                                                  const int32_t* free_pages, int64_t free_capacity,
+                                                  const int32_t* n_free, int32_t* n_free_out, int32_t* page_table,
+                                                  int32_t max_pages_per_seq, int64_t max_tokens, int32_t* seq_ids,
+                                                  int32_t* positions, int64_t* slots, int32_t* offsets,
+                                                  void* stream);
 
 /* spectra_release_pages -- give back the pages of finished sequences: for every
  * b with finished[b] != 0, in the order of (b, k), page_table[b][k] for k in

@@ -86,6 +86,8 @@ _SIGS = {
     "spectra_decode_attend_shared": [_vp, _P(CacheDesc), _vp, _vp, _i32, _vp, _vp, _sz, _vp],
     "spectra_planner_create": [_i32, _P(_vp)],
     "spectra_plan_append": [_vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp],
+    "spectra_plan_append_ex": [_vp, _i32, _vp, _vp, _vp, _i32, _vp, _i64, _vp, _vp, _vp, _i32, _i64, _vp, _vp, _vp, _vp,
+                               _vp],
     "spectra_release_pages": [_vp, _i32, _vp, _vp, _i32, _vp, _i32, _vp, _i64, _vp, _vp],
     "spectra_planner_status": [_vp, _vp],
     "spectra_rope_frequencies": [_P(RopeDesc), _i32, _vp, _P(ctypes.c_double)],

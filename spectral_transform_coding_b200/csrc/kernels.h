@@ -184,8 +184,8 @@ cudaError_t launch_rope(const RopeFreq& f, bool bf16, int d_head, const int32_t*
 // plan_kernels.cu
 constexpr int kPlanMaxBatch = 16384;
 cudaError_t launch_plan_append(int P, int32_t* err, int batch, const int32_t* lengths, const int32_t* new_tokens,
-                               const int32_t* prefix, int n_prefix, const int32_t* free_pages, const int32_t* n_free,
-                               int32_t* n_free_out, int32_t* table, int max_pages, int64_t max_tokens,
+                               const int32_t* prefix, int n_prefix, const int32_t* free_pages, int64_t free_capacity,
+                               const int32_t* n_free, int32_t* n_free_out, int32_t* table, int max_pages, int64_t max_tokens,
                                int32_t* seq_ids, int32_t* positions, int64_t* slots, int32_t* offsets,
                                cudaStream_t st);
 cudaError_t launch_release_pages(int P, int32_t* err, int batch, const int32_t* finished, int32_t* lengths,

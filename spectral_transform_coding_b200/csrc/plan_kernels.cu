@@ -91,7 +91,7 @@ struct PlanArgs {
   const int32_t *lengths, *new_tokens, *prefix, *free_pages, *n_free;
   int32_t *n_free_out, *table, *seq_ids, *positions, *offsets, *err;
   int64_t* slots;
-  int64_t max_tokens;
+  int64_t max_tokens, free_capacity;
   int batch, n_prefix, max_pages, P;
   bool wide;  // the tokens' outputs take 16-byte stores
 };
@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_append_kernel(const PlanArg
       first_s[b] = (int)at.pg;
     }
   }
+  if (n_free > A.free_capacity) bad |= 1;  // (its top lies outside the array)
   if (carry.tok > A.max_tokens || n_free < 0 || carry.pg == kMost || carry.pg > (uint32_t)n_free) bad |= 2;
   if (tid == 0) {
     off_s[B] = (int)carry.tok;
@@ -298,12 +299,12 @@ cudaError_t launch_plan(void (*kern)(const Args), const Args& a, int batch, int6
 }  // namespace
 
 cudaError_t launch_plan_append(int P, int32_t* err, int batch, const int32_t* lengths, const int32_t* new_tokens,
-                               const int32_t* prefix, int n_prefix, const int32_t* free_pages, const int32_t* n_free,
-                               int32_t* n_free_out, int32_t* table, int max_pages, int64_t max_tokens,
+                               const int32_t* prefix, int n_prefix, const int32_t* free_pages, int64_t free_capacity,
+                               const int32_t* n_free, int32_t* n_free_out, int32_t* table, int max_pages, int64_t max_tokens,
                                int32_t* seq_ids, int32_t* positions, int64_t* slots, int32_t* offsets,
                                cudaStream_t st) {
   const PlanArgs a{lengths, new_tokens, prefix,  free_pages, n_free, n_free_out, table, seq_ids, positions,
-                   offsets, err,        slots,   max_tokens, batch,  n_prefix,   max_pages, P,
+                   offsets, err,        slots,   max_tokens, free_capacity, batch, n_prefix, max_pages, P,
                    ((reinterpret_cast<uintptr_t>(seq_ids) | reinterpret_cast<uintptr_t>(positions) |
                      reinterpret_cast<uintptr_t>(slots)) & 15) == 0};
   // runs of four tokens only where there are more than threads: a run that spans sequences

@@ -105,9 +105,21 @@ spectra_status spectra_plan_append(const spectra_planner* p, int32_t batch, cons
                                    int32_t* page_table, int32_t max_pages_per_seq, int64_t max_tokens,
                                    int32_t* seq_ids, int32_t* positions, int64_t* slots, int32_t* offsets,
                                    void* stream) {
+  return spectra_plan_append_ex(p, batch, lengths, new_tokens, prefix_pages, n_prefix, free_pages, INT32_MAX, n_free,
+                                n_free_out, page_table, max_pages_per_seq, max_tokens, seq_ids, positions, slots,
+                                offsets, stream);
+}
+
+spectra_status spectra_plan_append_ex(const spectra_planner* p, int32_t batch, const int32_t* lengths,
+                                      const int32_t* new_tokens, const int32_t* prefix_pages, int32_t n_prefix,
+                                      const int32_t* free_pages, int64_t free_capacity, const int32_t* n_free,
+                                      int32_t* n_free_out, int32_t* page_table, int32_t max_pages_per_seq,
+                                      int64_t max_tokens, int32_t* seq_ids, int32_t* positions, int64_t* slots,
+                                      int32_t* offsets, void* stream) {
   return guarded([&]() -> spectra_status {
     if (!p || !lengths || !new_tokens || !free_pages || !n_free || !n_free_out || !page_table || !offsets)
       return fail(SPECTRA_ERR_INVALID, "null pointer");
+    if (free_capacity < 0 || free_capacity > INT32_MAX) return fail(SPECTRA_ERR_INVALID, "free_capacity out of range");
     if (max_tokens < 0 || max_tokens > (1 << 24)) return fail(SPECTRA_ERR_INVALID, "max_tokens out of range");
     if (max_tokens > 0 && !seq_ids) return fail(SPECTRA_ERR_INVALID, "null pointer");
     if (n_prefix > 0 && !prefix_pages) return fail(SPECTRA_ERR_INVALID, "null pointer");
@@ -118,7 +130,7 @@ spectra_status spectra_plan_append(const spectra_planner* p, int32_t batch, cons
     const spectra_status s = check_batch(p, batch, n_prefix, max_pages_per_seq);
     if (s != SPECTRA_OK) return s;
     CUDA_TRY(launch_plan_append(p->page_tokens, p->err, batch, lengths, new_tokens, prefix_pages, n_prefix, free_pages,
-                                n_free, n_free_out, page_table, max_pages_per_seq, max_tokens, seq_ids, positions,
+                                free_capacity, n_free, n_free_out, page_table, max_pages_per_seq, max_tokens, seq_ids, positions,
                                 slots, offsets, static_cast<cudaStream_t>(stream)));
     return SPECTRA_OK;
   });

@@ -149,7 +149,8 @@ class PagePlanner:
     def plan_append(self, page_table, lengths, new_tokens, free_pages, n_free, prefix_pages=None, n_free_out=None,
                     plan=None, max_tokens=None, stream=None) -> AppendPlan:
         """Pages, sequence ids, positions and slots of the next append (``spectra_plan_append``): updates
-        ``page_table`` and ``n_free`` (or writes ``n_free_out``) and fills ``plan``.  Rows of the plan behind the
+        ``page_table`` and ``n_free`` (or writes ``n_free_out``) and fills ``plan``; an ``n_free`` above the size of
+        ``free_pages`` is an error that ``status`` raises.  Rows of the plan behind the
         last token hold -1; ``Rope.apply`` passes over them, an append takes ``seq_ids[:number of tokens]``."""
         torch = _torch()
         i32 = torch.int32
@@ -178,12 +179,11 @@ class PagePlanner:
                     _fresh(t, st)
             elif plan.batch != B:
                 raise ValueError("the plan was made for another batch")
-            check(lib.spectra_plan_append(
-                self._h, B, lengths.data_ptr(), new_tokens.data_ptr(),
-                prefix_pages.data_ptr() if n_prefix else None, n_prefix, free_pages.data_ptr(), n_free.data_ptr(),
-                n_free_out.data_ptr(), page_table.data_ptr(), most, plan.max_tokens, plan.seq_ids.data_ptr(),
-                plan.positions.data_ptr(), plan.slots.data_ptr(), plan.offsets.data_ptr(), st.raw),
-                "spectra_plan_append")
+            check(lib.spectra_plan_append_ex(
+                self._h, B, lengths.data_ptr(), new_tokens.data_ptr(), prefix_pages.data_ptr() if n_prefix else None,
+                n_prefix, free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(), n_free_out.data_ptr(),
+                page_table.data_ptr(), most, plan.max_tokens, plan.seq_ids.data_ptr(), plan.positions.data_ptr(),
+                plan.slots.data_ptr(), plan.offsets.data_ptr(), st.raw), "spectra_plan_append_ex")
         return plan
 
     def release(self, page_table, lengths, finished, free_pages, n_free, n_prefix: int = 0, stream=None):
