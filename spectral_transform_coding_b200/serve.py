@@ -109,15 +109,33 @@ def _copied(x, st):
 
 
 class AppendPlan:
-    """Output tensors of ``PagePlanner.plan_append`` for up to ``max_tokens`` tokens of ``batch`` sequences."""
+    """Output tensors of ``PagePlanner.plan_append`` for up to ``max_tokens`` tokens of ``batch`` sequences.
+
+    Other tensors of the same type, size and device may be put in their place."""
 
     def __init__(self, max_tokens: int, batch: int, device="cuda"):
         torch = _torch()
-        self.max_tokens, self.batch = int(max_tokens), int(batch)
-        self.seq_ids = torch.empty(self.max_tokens, dtype=torch.int32, device=device)
-        self.positions = torch.empty(self.max_tokens, dtype=torch.int32, device=device)
-        self.slots = torch.empty(self.max_tokens, dtype=torch.int64, device=device)
-        self.offsets = torch.empty(self.batch + 1, dtype=torch.int32, device=device)
+        self._max_tokens, self._batch = int(max_tokens), int(batch)
+        T, self._tensors = self._max_tokens, {}
+        for name, n, dtype in (("seq_ids", T, torch.int32), ("positions", T, torch.int32), ("slots", T, torch.int64),
+                               ("offsets", self._batch + 1, torch.int32)):
+            self._tensors[name] = torch.empty(n, dtype=dtype, device=device)
+
+    max_tokens = property(lambda self: self._max_tokens)
+    batch = property(lambda self: self._batch)
+
+    def _put(self, name, t):
+        old = self._tensors[name]
+        if t.dtype != old.dtype:
+            raise TypeError(f"{name} must be {old.dtype}")
+        if t.shape != old.shape or not t.is_contiguous() or t.device != old.device:
+            raise ValueError(f"{name} must be contiguous, of shape {tuple(old.shape)} and on {old.device}")
+        self._tensors[name] = t
+
+    seq_ids = property(lambda self: self._tensors["seq_ids"], lambda self, t: self._put("seq_ids", t))
+    positions = property(lambda self: self._tensors["positions"], lambda self, t: self._put("positions", t))
+    slots = property(lambda self: self._tensors["slots"], lambda self, t: self._put("slots", t))
+    offsets = property(lambda self: self._tensors["offsets"], lambda self, t: self._put("offsets", t))
 
 
 class PagePlanner:
