@@ -815,10 +815,11 @@ spectra_status spectra_reconstruct(const spectra_codec* c, const spectra_cache* 
 spectra_status spectra_device_status(const spectra_codec* c, void* stream) {
   if (!c) return fail(SPECTRA_ERR_INVALID, "null codec");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  CUDA_TRY(cudaStreamSynchronize(st));
+  // in `stream` alone, and cleared before the return: a later call's error in another stream stays
   int32_t v = 0;
-  CUDA_TRY(cudaMemcpy(&v, c->err, 4, cudaMemcpyDeviceToHost));
-  CUDA_TRY(cudaMemset(c->err, 0, 4));
+  CUDA_TRY(cudaMemcpyAsync(&v, c->err, 4, cudaMemcpyDeviceToHost, st));
+  CUDA_TRY(cudaMemsetAsync(c->err, 0, 4, st));
+  CUDA_TRY(cudaStreamSynchronize(st));
   if (v == 0) return SPECTRA_OK;
   return fail(static_cast<spectra_status>(v), "device-side error recorded by a kernel");
 }

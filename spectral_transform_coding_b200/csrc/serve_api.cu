@@ -84,6 +84,7 @@ spectra_status spectra_planner_create(int32_t page_tokens, spectra_planner** out
     cudaError_t e = cudaGetDevice(&p->device);
     if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&p->err), 256);
     if (e == cudaSuccess) e = cudaMemset(p->err, 0, 256);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);  // (the planner's streams may not wait for it)
     if (e != cudaSuccess) {
       spectra_planner_destroy(p);
       return fail(SPECTRA_ERR_CUDA, std::string("planner: ") + cudaGetErrorString(e));
@@ -160,10 +161,11 @@ spectra_status spectra_planner_status(const spectra_planner* p, void* stream) {
   return guarded([&]() -> spectra_status {
     if (!p) return fail(SPECTRA_ERR_INVALID, "null planner");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    CUDA_TRY(cudaStreamSynchronize(st));
+    // in `stream` alone, and cleared before the return: a later call's error in another stream stays
     int32_t v = 0;
-    CUDA_TRY(cudaMemcpy(&v, p->err, 4, cudaMemcpyDeviceToHost));
-    CUDA_TRY(cudaMemset(p->err, 0, 4));
+    CUDA_TRY(cudaMemcpyAsync(&v, p->err, 4, cudaMemcpyDeviceToHost, st));
+    CUDA_TRY(cudaMemsetAsync(p->err, 0, 4, st));
+    CUDA_TRY(cudaStreamSynchronize(st));
     if (v == 0) return SPECTRA_OK;
     return fail(static_cast<spectra_status>(v), v == SPECTRA_ERR_CAPACITY
                                                     ? "too few free pages, table entries or token slots"
