@@ -32,6 +32,12 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 // before pdl_wait touch only read-only codec data and the caller's inputs; read
 // predecessor outputs and write any shared buffer after it; and call pdl_wait
 // before exiting, so that each kernel's completion implies all earlier ones'.
+// One exception: the decode kernel behind the prefix kernel (AttendArgs::late_wait)
+// waits only before it merges.  Every CTA of the prefix kernel has passed its own wait
+// before it lets this grid start, so all that came before it is complete and its
+// writes are in L2, and it writes nothing that the decode kernel reads sooner (nor
+// reads what that one writes); but no wait of this grid stands between those writes
+// and its loads, so they bypass L1 (__ldcg, or bulk copies).
 // Without the launch attribute both are no-ops.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
