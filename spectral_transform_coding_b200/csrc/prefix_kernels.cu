@@ -90,10 +90,10 @@ constexpr int kPfBars = 0;       // uint64 [kPfMaxStages + 4]: pages, S, O, drai
 constexpr int kPfMisc = 320;     // int: TMEM address, stop flag, pages of this CTA, K steps and positions with low parts
 constexpr int kPfOrd = 384;      // int4 [2][kMaxG] groups in width-class order {block off, record off, group, width}
 constexpr int kPfOffs = 640;      // float [4][128] kPfOff - m of each row (added to a score), a copy per token quarter
-constexpr int kPfFac = 2688;      // float [4][128] the factors of a rescaling
-constexpr int kPfWMax = 4736;     // float [4][128] maxima, then sums, by token quarter
-constexpr int kPfOver = 6784;     // int [2][128] maxima above the limit, ordered as integers
-constexpr int kPfLane = 7808;     // uint4 [2][kMaxG][32] lane tables of the groups (width 8: not read)
+constexpr int kPfWMax = 2688;     // float [4][128] by token quarter: the first tile's maxima, after the last the sums
+constexpr int kPfFac = kPfWMax;   // (between) float [4][128] a warp's own: the factors of a rescaling
+constexpr int kPfOver = 4736;     // int [2][128] maxima above the limit, ordered as integers
+constexpr int kPfLane = 5760;     // uint4 [2][kMaxG][32] lane tables of the groups (width 8: not read)
 constexpr int kPfPos = kPfLane + 2 * kMaxG * 512;  // K groups: int [8] record offsets by position, int [8] bytes to the
                                                    // low parts' chunks in class order, int [8] the steps of 16
                                                    // coordinates with low parts
@@ -877,7 +877,7 @@ __global__ void __launch_bounds__(32 * W + 32, CTAS) prefix_kernel(const __grid_
         const float fac = m == m_run ? 1.f : (m_run == -CUDART_INF_F ? 0.f : attend::ex2_approx(m_run - m));
         if (lane % kLc == 0) {
           off_w[lane / kLc] = off_new;
-          fac_w[lane / kLc] = fac;
+          if (t > 0) fac_w[lane / kLc] = fac;  // (the first tile's maxima may still be read)
         }
         const uint32_t moved = __ballot_sync(0xffffffffu, m != m_run && lane % kLc == 0);
         m_run = m;
@@ -1013,7 +1013,7 @@ struct PrefixSmem {
   int off_k, off_q, off_p, off_ring, stage_bytes, stages, total, fold_dims;
 };
 
-constexpr int kPfSmemMax = 226 * 1024;  // of a CTA that has an SM for itself
+constexpr int kPfSmemMax = 227 * 1024;  // of a CTA that has an SM for itself
 
 // V, K, Q, P, and as many page stages as leave room for two CTAs per SM, else for one: two tiles'
 // pages at least, eight tiles' at most.
@@ -1047,7 +1047,7 @@ PrefixSmem prefix_smem(const CodecDev& h, int n_cols) {
 // Fewer columns cost fewer score and exp2 instructions a token; in blocks of 64 rows 64
 // sequences x 28k at 4x unpacked every code four times and took 239 us, in blocks of 128 165 us.
 // Fewer where two tiles' pages would not fit beside the operands (many wide groups; 32 always fit:
-// 8 groups of 16 at 8 bits on both sides, the most there is, take 227,072 bytes).
+// 8 groups of 16 at 8 bits on both sides, the most there is, take 225,024 bytes).
 int prefix_columns(const CodecDev& h, int rows) {
   int n = rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128));
   while (n > 32 && prefix_smem(h, n).total > kPfSmemMax) n /= 2;
