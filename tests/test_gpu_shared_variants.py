@@ -43,3 +43,30 @@ def test_variant(monkeypatch, name, batch, variant):
     seen = [re.search(r"prefix_kernel<(.*?)>", e.name) for e in prof.events()]
     seen = [tuple(int(x) for x in re.findall(r"\d+", re.sub(r"\(int\)", "", m.group(1)))) for m in seen if m]
     assert seen and set(seen) == {variant}
+
+
+@pytest.mark.parametrize("name,page", [("toy", 0), ("toy", 3), ("toy", 9), ("llama4x", 4)])
+def test_bounded_wait_with_128_rows_a_block(monkeypatch, name, page):
+    """A page copy that never lands, where the keys are unpacked behind the softmax: the call reports a timeout, and the
+    next calls with the same workspace give the exact result."""
+    torch = torch_mod()
+    import spectral_transform_coding_b200 as st
+    s = base._codec(name, 14)
+    cache, table, prefix, lengths = base._filled(s, 900, [5] * 33, 14)
+    q, _ = base._queries(s, 33, 14)
+    codec = s["codec"]
+    ws = torch.zeros(codec.decode_shared_workspace_bytes(33), dtype=torch.uint8, device=q.device)
+    out = codec.decode_attend_shared(cache, q, prefix, workspace=ws)
+    codec.device_status()
+    monkeypatch.setenv("SPECTRA_PREFIX_TEST_DROP_PAGE", str(page))
+    monkeypatch.setenv("SPECTRA_DECODE_TEST_WAIT_NS", "2000000")
+    codec.decode_attend_shared(cache, q, prefix, workspace=ws)
+    with pytest.raises(st.SpectraError) as e:
+        codec.device_status()
+    assert e.value.status == 6
+    monkeypatch.delenv("SPECTRA_PREFIX_TEST_DROP_PAGE")
+    monkeypatch.delenv("SPECTRA_DECODE_TEST_WAIT_NS")
+    for _ in range(2):
+        got = codec.decode_attend_shared(cache, q, prefix, workspace=ws)
+        codec.device_status()
+        assert torch.equal(got, out)
