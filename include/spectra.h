@@ -418,11 +418,12 @@ SPECTRA_API spectra_status spectra_decode_shared_workspace_bytes(const spectra_c
  *       aligned; zero it once before its first use, every call leaves its
  *       counters at zero (as spectra_decode_attend's, which it may share).  Calls
  *       that share a workspace must not overlap.
- * Precision: over the shared pages scores come from the exact keys and folded
- * queries of 22 bits, as in spectra_decode_attend; softmax weights and value
+ * Precision: over the shared pages scores come from the exact keys, as in
+ * spectra_decode_attend, and queries folded with W_up of 16 bits; softmax weights and value
  * latents enter the tensor cores as fp16, and every sum is fp32 (see
- * prefix_kernels.cu).  Dequantised latents, and a group's sum of a folded query
- * (in log2 units over sqrt(d_head)), must fit fp16 (+-65504).  The result is
+ * prefix_kernels.cu).  Dequantised latents, a token's spread within a group of keys
+ * and a group's sum of a folded query (in log2 units over sqrt(d_head)) must fit
+ * fp16 (+-65504).  The result is
  * deterministic.  q is read after the dependency on earlier launches resolves,
  * so a kernel of this library may have written it.
  * A length outside [0, max_pages_per_seq * page_tokens] or in (0, n_prefix *

@@ -19,9 +19,9 @@
 //   1. unpack: a lane's 8 codes of a (block, group) come as fp16 integers by one
 //      and/or (code | 0x6400 = 1024 + code, or code << 4 | 0x5400 = 64 + code), one
 //      subtraction and one product with the token's scale.  Values: c = rn(code s + z),
-//      one fma, rounded once.  Keys exactly, as decode_attend's: c = (code - 2) s + 2 s + z,
-//      where (code - 2) s is an fp16 number for widths 1 and 2 (-2 s .. s) and the sum of two
-//      for the others (the second ones are further coordinates of the row), and 2 s and z of
+//      one fma, rounded once.  Keys exactly, as decode_attend's: c = (code - 1) s + s + z,
+//      where (code - 1) s is an fp16 number for widths 1 and 2 (-s .. 2 s) and the sum of two
+//      for the others (the second ones are further coordinates of the row), and s and z of
 //      each group are two more coordinates, against the sum of the group's q_lat.
 //      The packed layout is that of MMA fragments, so four lanes hold 8
 //      adjacent coordinates of a token (K) or 8 adjacent tokens of a coordinate (V) and
@@ -124,11 +124,11 @@ struct PrefixArgs {
 };
 
 // 16-byte chunks of 8 coordinates of a K row, whole MMA steps of 16:
-//   [kept coordinates, at least a step] [z of 8 groups | 2 s of 8 groups] [low parts of wide groups]
+//   [kept coordinates, at least a step] [z of 8 groups | s of 8 groups] [low parts of wide groups]
 // and of a Q row: [q_lat's high parts | its groups' sums twice] [low parts of both].
 __host__ __device__ inline int main_chunks(int kept) { return kept > 0 ? (kept + 15) / 16 * 2 : 2; }
 __host__ __device__ inline int q_chunks(int kept) { return 2 * (main_chunks(kept) + 2); }
-// Widths whose (code - 2) s has more bits than fp16 (width 2: -2 s .. s).
+// Widths whose (code - 1) s has more bits than fp16 (width 2: -s .. 2 s).
 __host__ __device__ inline bool wide_code(int b) { return b >= 3; }
 
 __device__ __forceinline__ void st_s32(uint32_t a, uint32_t v) {
@@ -138,7 +138,7 @@ __device__ __forceinline__ void st_s128(uint32_t a, uint32_t x, uint32_t y, uint
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// The lane's 8-bit codes (K side: less 2) of one block (half `odd` of a 32-token block for G = 8) as
+// The lane's 8-bit codes (K side: less 1) of one block (half `odd` of a 32-token block for G = 8) as
 // four registers of two fp16 integers each, fragment order (registers 1 and 3: rows + 8).
 template <int G>
 __device__ __forceinline__ void load_bytes(uint32_t blk, int side, int odd, __half2 (&c)[4]) {
@@ -161,7 +161,7 @@ __device__ __forceinline__ void load_bytes(uint32_t blk, int side, int odd, __ha
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     r[i] = (r[i] & 0x00FF00FFu) | 0x64006400u;
-    c[i] = __hsub2(*reinterpret_cast<__half2*>(&r[i]), __float2half2_rn(side == 0 ? 1026.f : 1024.f));
+    c[i] = __hsub2(*reinterpret_cast<__half2*>(&r[i]), __float2half2_rn(side == 0 ? 1025.f : 1024.f));
   }
 }
 
@@ -268,7 +268,7 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, lon
 // Groups c .. c + U - 1 (past n_end: that one again, the same bytes to the same place) of a
 // block, all of width 4, 2 or 1, or all of width 3 (B3), from the lane table
 // `tab`: the loads of all of them first, then the arithmetic and the stores.
-// K side (SIDE 0): (code - 2) s of coordinates 2 t4 (+ 8) of an even token (dst) and an odd
+// K side (SIDE 0): (code - 1) s of coordinates 2 t4 (+ 8) of an even token (dst) and an odd
 // one (dst2), of the groups before n_lo in two parts, the low ones at their groups' offsets
 // `lo`; V side: c = rn(code s + z) of coordinates gid (+ 8) of token pairs t4 and t4 + 4.
 template <int G, int SIDE, int U, bool B3>
@@ -289,7 +289,7 @@ __device__ __forceinline__ void unpack_batch(uint32_t tab, int c, int n_end, uin
     if (SIDE == 1) ra[u] = ld_s64(sec + d[u].y + rec);
     if (SIDE == 1) rb[u] = ld_s64(sec + d[u].y + rec + (uint32_t)(32 * tpp));
   }
-  const __half2 h1024 = __float2half2_rn(SIDE == 0 ? 1026.f : 1024.f), h64 = __float2half2_rn(SIDE == 0 ? 66.f : 64.f);
+  const __half2 h1024 = __float2half2_rn(SIDE == 0 ? 1025.f : 1024.f), h64 = __float2half2_rn(SIDE == 0 ? 65.f : 64.f);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     {
@@ -390,7 +390,7 @@ __device__ __forceinline__ void unpack_block(const int4* ord, uint32_t tab, int 
   }
 }
 
-// z and 2 s of every K group of a 16-token block: lane (pair of groups lane >> 3, pair of
+// z and s of every K group of a 16-token block: lane (pair of groups lane >> 3, pair of
 // tokens lane & 7); zeros for the groups that there are not.  dst: the z chunk's row of the even
 // token, dst2: of the odd one.
 __device__ __forceinline__ void unpack_offsets(uint32_t pos, int n_groups, uint32_t sec, int blk16, int tpp, int lane,
@@ -401,12 +401,11 @@ __device__ __forceinline__ void unpack_offsets(uint32_t pos, int n_groups, uint3
   uint2 a = make_uint2(0u, 0u), b = a;
   if (p < n_groups) a = ld_s64(at + off.x);
   if (p + 1 < n_groups) b = ld_s64(at + off.y);
-  const uint32_t sa = bits_of(__hadd2(as_half2(a.x), as_half2(a.x))), sb = bits_of(__hadd2(as_half2(b.x), as_half2(b.x)));
   const uint32_t word = (uint32_t)(lane >> 3) * 4u;
   st_s32(dst + word, __byte_perm(a.y, b.y, 0x5410));
   st_s32(dst2 + word, __byte_perm(a.y, b.y, 0x7632));
-  st_s32(dst + word + 128u, __byte_perm(sa, sb, 0x5410));
-  st_s32(dst2 + word + 128u, __byte_perm(sa, sb, 0x7632));
+  st_s32(dst + word + 128u, __byte_perm(a.x, b.x, 0x5410));
+  st_s32(dst2 + word + 128u, __byte_perm(a.x, b.x, 0x7632));
 }
 
 template <int G, int NB, int W, int CTAS>
@@ -581,7 +580,7 @@ __global__ void __launch_bounds__(32 * W + 32, CTAS) prefix_kernel(const __grid_
         if (tc::elect()) {
           const uint32_t d = tmem + kS + (uint32_t)(((t + 1) & 1) * NB);
 #pragma unroll 1
-          for (int k = 0; k <= n_main; ++k) {  // the last: z and 2 s
+          for (int k = 0; k <= n_main; ++k) {  // the last: z and s
             tc::mma(d, dK + (uint64_t)(k * 16), dQ + (uint64_t)(k * 16), kIdS, k > 0);
             tc::mma(d, dK + (uint64_t)(k * 16), dQ + (uint64_t)((n_main + 1 + k) * 16), kIdS, true);
           }
@@ -724,7 +723,7 @@ __global__ void __launch_bounds__(32 * W + 32, CTAS) prefix_kernel(const __grid_
           const uint32_t at_c = at_sum + (uint32_t)((c >> 3) * cq * 128 + (c & 7) * 16);
           const float sum = g < nK ? v[i] : 0.f;
           st_two_parts(at_c, low, sum);         // times z
-          st_two_parts(at_c + 128u, low, sum);  // times 2 s
+          st_two_parts(at_c + 128u, low, sum);  // times s
         }
       }
     }
@@ -998,7 +997,7 @@ PrefixKernel prefix_kernel_of(int n_cols, int ctas, int* warps) {
   }
 }
 
-// Chunks of a K row of head `hd`: kept coordinates, z and 2 s, a step for each with a wide group.
+// Chunks of a K row of head `hd`: kept coordinates, z and s, a step for each with a wide group.
 int k_chunks(const CodecDev& h, const HeadDev& hd) {
   const SideDev& k = hd.side[0];
   uint32_t steps = 0;

@@ -30,9 +30,17 @@ def _with_latents(s, n_prefix, own, lat, seed):
     return cache, table, torch.from_numpy(ids[:n_prefix]).to(dev()), cache.lengths.cpu().numpy()
 
 
-def _bar(s, cache, table, lengths, q, outs):
+def _two_bf16(W):
+    """W as the fold of the queries takes it: two bf16 parts, 2^-17 of each entry left out."""
+    torch = torch_mod()
+    x = torch.from_numpy(np.ascontiguousarray(W, np.float32))
+    hi = x.to(torch.bfloat16).float()
+    return (hi.double() + (x - hi).to(torch.bfloat16).double()).numpy()
+
+
+def _bar(s, cache, table, lengths, q, outs, fold=lambda W: W):
     """Largest error of each of `outs` [batch][heads][d_head] in units of the bar."""
-    W = kept_wup(s["W_up"], s["widths"], s["group"])
+    W = [[fold(K), V] for K, V in kept_wup(s["W_up"], s["widths"], s["group"])]
     gq = s["n_q"] // s["n_kv"]
     s.pop("pool", None)
     worst = np.zeros(len(outs))
@@ -104,6 +112,34 @@ def test_keys_far_from_zero(name):
     assert worst[2] <= 1.0
     assert worst[1] <= 1.0
     assert worst[0] <= 1.0
+
+
+@pytest.mark.parametrize("name", ["llama4x", "qwen8x", "allwidths"])
+def test_keys_that_differ_by_most_of_the_range_of_fp16(name):
+    """The last kept group of keys (1 bit; allwidths: also 8 bits) with spreads of about 60,000, and queries nearly
+    orthogonal to it. Queries' low parts end at 2^-25: 2^-25 * 16 * 30000 / sqrt(128) = 1.3e-3 in a score at most. The
+    fold's parts of W_up leave 2^-17 * 16 * 30000 * sum_d |q_d W_kd| (about 0.3) / sqrt(128) = 0.1 at most, several 1e-3
+    in this case (the products of one sign cancel, what is left of them does not): the reference takes the same parts."""
+    s = _codec(name, 51)
+    codec, P = s["codec"], s["P"]
+    kept = kept_wup(s["W_up"], s["widths"], s["group"])
+    lat = synthetic_latents(6 * P, codec.n_eff, seed=52, decay=0.2)
+    rng = np.random.default_rng(53)
+    q, col = rng.standard_normal((2, s["n_q"], s["d_h"])), 0
+    gq = s["n_q"] // s["n_kv"]
+    for a in range(s["n_kv"]):
+        nK, g = len(kept[a][0]), s["group"]
+        lat[:, col + nK - g:col + nK] = rng.uniform(-30000, 30000, (len(lat), g))
+        W = np.asarray(kept[a][0][nK - g:], np.float64)
+        rows = slice(a * gq, (a + 1) * gq)
+        q[:, rows] -= (q[:, rows] @ W.T) @ W
+        col += nK + len(kept[a][1])
+    torch = torch_mod()
+    q = torch.from_numpy((0.05 * q).astype(np.float32)).to(dev()).to(torch.bfloat16)
+    cache, table, prefix, lengths = _with_latents(s, 6, [lat[5:40], lat[:0]], lat, 54)
+    out = codec.decode_attend_shared(cache, q, prefix)
+    codec.device_status()
+    assert _bar(s, cache, table, lengths, q.double().cpu().numpy(), [out.double().cpu().numpy()], _two_bf16)[0] <= 1.0
 
 
 @pytest.mark.parametrize("own", [[0, 0], [0, 7], [70, 0]])
