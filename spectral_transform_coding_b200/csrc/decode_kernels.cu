@@ -45,6 +45,16 @@
 
 namespace spectra {
 
+int sm_count() {
+  static int n = 0;
+  if (n == 0) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+  }
+  return n;
+}
+
 namespace {
 
 using attend::AttendArgs;
@@ -56,16 +66,6 @@ using attend::kMaxKept;
 using attend::kMaxSplit;
 using attend::kOffFixedEnd;
 using attend::kCpStride;
-
-int sm_count() {
-  static int n = 0;
-  if (n == 0) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-  }
-  return n;
-}
 
 // Tiles (16 tokens) per softmax chunk: 4 when a page holds a multiple of 64
 // tokens, else 2 (pages hold a multiple of 32).

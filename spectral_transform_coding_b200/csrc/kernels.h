@@ -128,6 +128,7 @@ cudaError_t launch_decode_reconstruct(const CodecDev& h, const CodecDev* d, cons
                                       const RtPlan& plan, cudaStream_t st);
 
 // decode_kernels.cu
+int sm_count();  // of the current device at the first call
 // Raises `kern`'s dynamic shared-memory limit on the current device to at least
 // `bytes` (one record per kernel and device; the limit never shrinks).
 cudaError_t ensure_dynamic_smem(const void* kern, int bytes);

@@ -15,8 +15,8 @@
 // Measured: 65536 tokens of 28 + 4 heads of 128 in bf16 take 174 us, 6.17 TB/s (94 % of
 // a copy's rate); batches of two heads 199 us, items (token, head, vector) dealt
 // out evenly with {c, s} read from the table for each 275 us, walks of
-// both tensors in registers at once 221-241 us.  4097 tokens of 32 + 8 heads of 64 in fp32
-// take 19 us.  A decode step (16 tokens of 32 + 8 heads) takes 3.7 us, of which
+// both tensors in registers at once 221-241 us.  4097 tokens of 8 + 8 heads of 128 in fp32,
+// 96 dimensions turned, take 19 us.  A decode step (16 tokens of 32 + 8 heads) takes 3.7 us, of which
 // the launch and one round trip to memory are most.
 // Angles: turns of pi, position x frequency / pi, are formed in fp64 and reduced
 // to [-1, 1] there (fp32 has no digits left at position 10^6); the remainder goes
@@ -309,11 +309,11 @@ cudaError_t launch_rope(const RopeFreq& f, bool bf16, int d_head, const int32_t*
   // the GPU; a short call splits each token's heads over CTAs instead (each forms the
   // sincos again).
   int tok = 1;
-  while (tok < kRopeTokMax && 2 * tok * A.n_all <= kRopeThreads && (n_tokens + 2 * tok - 1) / (2 * tok) >= 4 * 148)
+  while (tok < kRopeTokMax && 2 * tok * A.n_all <= kRopeThreads && (n_tokens + 2 * tok - 1) / (2 * tok) >= 4 * sm_count())
     tok *= 2;
   const int64_t tiles = (n_tokens + tok - 1) / tok;
   int split = 1;
-  while (tiles * split < 148 && split * 2 <= heads) split *= 2;
+  while (tiles * split < sm_count() && split * 2 <= heads) split *= 2;
   A.tok = tok;
   A.split = split;
   A.lanes = kRopeThreads / (tok * A.n_all);
