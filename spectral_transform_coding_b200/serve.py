@@ -91,8 +91,7 @@ def _pair(name, x, out, T, d, like, st):
     torch = _torch()
     if out.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name}_out needs a gradient, which the call does not record")
-    if not out.is_inference():
-        torch.autograd.graph.increment_version(out)  # (a graph may hold it for its backward pass)
+    torch._C._increment_version((out,))  # (a graph may hold it for its backward pass)
     return given, given if out is x else _heads(name + "_out", out, n), out
 
 
