@@ -402,14 +402,16 @@ SPECTRA_API spectra_status spectra_decode_shared_workspace_bytes(const spectra_c
 
 /* spectra_decode_attend_shared -- one decode step of attention for a batch whose
  * sequences all begin with the same tokens (a system prompt, a document), the
- * shared pages read and attended once for the whole batch:
+ * shared pages read and unpacked once for every 128 query rows (sequence, q head of
+ * a KV head) instead of once for every sequence:
  *   out[b] = softmax(q[b] W_up^K^T c_K / sqrt(d_head)) c_V W_up^V
  * over the n_prefix * page_tokens tokens of the pages prefix_pages[0 .. n_prefix)
- * followed by the tokens [n_prefix * page_tokens, lengths[b]) of sequence b, the
- * same numbers as spectra_decode_attend over a page table whose rows begin with
- * prefix_pages.  The first n_prefix entries of the rows are not read here.  No
- * counterpart on the SPECTRA pages; the latent form is theirs ("Significance and
- * claims").
+ * followed by the tokens [n_prefix * page_tokens, lengths[b]) of sequence b, up to
+ * rounding the same numbers as spectra_decode_attend over a page table whose rows
+ * begin with prefix_pages.  That call is the faster one for few sequences or a
+ * short prefix (on a B200 mostly below 8 sequences, or below 8k shared tokens).
+ * The first n_prefix entries of the rows are not read here.  No counterpart on
+ * the SPECTRA pages; the latent form is theirs ("Significance and claims").
  *   q   device bf16 [batch][n_q_heads][d_head]
  *   prefix_pages device int32 [n_prefix] (may be NULL when n_prefix is 0)
  *   out device bf16 [batch][n_q_heads][d_head] (attention output before W_O); a
@@ -419,13 +421,16 @@ SPECTRA_API spectra_status spectra_decode_shared_workspace_bytes(const spectra_c
  *       counters at zero (as spectra_decode_attend's, which it may share).  Calls
  *       that share a workspace must not overlap.
  * Precision: over the shared pages scores come from the exact keys, as in
- * spectra_decode_attend, and queries folded with W_up of 16 bits; softmax weights and value
- * latents enter the tensor cores as fp16, and every sum is fp32 (see
- * prefix_kernels.cu).  Dequantised latents, a token's spread within a group of keys
- * and a group's sum of a folded query (in log2 units over sqrt(d_head)) must fit
- * fp16 (+-65504).  The result is
- * deterministic.  q is read after the dependency on earlier launches resolves,
- * so a kernel of this library may have written it.
+ * spectra_decode_attend, and queries folded with W_up of 16 bits; softmax
+ * weights and value latents enter the tensor cores as fp16, and every sum is
+ * fp32 (see prefix_kernels.cu).  Dequantised latents, a token's spread within a
+ * group of keys and a group's sum of a folded query (in log2 units over
+ * sqrt(d_head)) must fit fp16 (+-65504).  The result is deterministic.  q is read
+ * after the dependency on earlier launches resolves, so a kernel of this library
+ * may have written it.  The latent decodes turn nothing: q has rotary positions
+ * (spectra_rope_apply) only if the cached latents were made from keys that have
+ * them; over latents of keys without, as spectra_encode_append makes them of
+ * hidden states, positions go with spectra_decode_attend_reconstruct_rope.
  * A length outside [0, max_pages_per_seq * page_tokens] or in (0, n_prefix *
  * page_tokens) records SPECTRA_ERR_INVALID (that sequence gives 0); so does a
  * page id outside [0, n_pages) (that split's pages are skipped).  n_prefix must
@@ -456,9 +461,11 @@ SPECTRA_API void spectra_planner_destroy(spectra_planner* planner);
  *     read);
  *   offsets[b] = new_tokens[0] + .. + new_tokens[b-1], offsets[batch] the total;
  *   token i of the append, i < offsets[batch]: seq_ids[i] its sequence (the first
- *     offsets[batch] of them are what spectra_encode_append takes), positions[i] = lengths[b] + i - offsets[b]
- *     (what spectra_rope_apply takes), slots[i] = page * P + positions[i] % P,
- *     its place in the pool; all three are -1 for offsets[batch] <= i < max_tokens.
+ *     offsets[batch] of them are what spectra_encode_append takes, which refuses the
+ *     -1 behind them: a captured step of fixed size holds live slots alone),
+ *     positions[i] = lengths[b] + i - offsets[b] (what spectra_rope_apply takes),
+ *     slots[i] = page * P + positions[i] % P, its place in the pool; all three are
+ *     -1 for offsets[batch] <= i < max_tokens.
  * A sequence behind a shared prefix starts with lengths[b] = n_prefix * P.  The
  * lengths are not changed: the append advances them.
  *   lengths, new_tokens device int32 [batch]; prefix_pages device int32

@@ -281,7 +281,8 @@ class Codec:
 
     def decode_attend_shared(self, cache: "LatentCache", q, prefix_pages, out=None, workspace=None, stream=None):
         """Decode attention of a batch that shares the pages ``prefix_pages`` (int32 [n_prefix], on the GPU)
-        as the beginning of every sequence; q and out bf16 [batch][n_q_heads][d_head]."""
+        as the beginning of every sequence; q and out bf16 [batch][n_q_heads][d_head].  Mostly faster than
+        ``decode_attend`` from 8 sequences and 8k shared tokens on."""
         torch = _torch()
         shape = (cache.batch, self.cfg.n_q_heads, self.cfg.d_head)
         _check_tensor("q", q, torch.bfloat16, shape)

@@ -11,10 +11,10 @@
 // of the lengths and the first write to them.  Every CTA reaches the same verdict
 // on the checks (same inputs), so a refused call writes nothing.
 // Measured, one token for each of 1 / 16 / 256 / 1024 / 4096 sequences behind 16 shared
-// pages: 3.7 / 3.8 / 4.6 / 6.0 / 11.9 us (launch, scan and a chain of three loads); 65536
-// tokens of 48 prompts 9.4 us.  With sums of 64 bits that every thread added over the
-// warps by itself, and whole CTAs instead of warps dealt out, 1024 sequences took 8.9 us and the
-// prompts 11.3 us.
+// pages: 3.7 / 3.8 / 4.8 / 6.8 / 12.6 us in a captured row of calls (launch, scan and a chain of
+// three loads); 65536 tokens of 48 prompts 10.2 us.  With sums of 64 bits that every thread added over the
+// warps by itself, and whole CTAs instead of warps dealt out, 1024 sequences took 2.9 us more and the
+// prompts 1.9 us more.  Releasing 1024 sequences of 64 pages takes 10 us, 16 of 512 pages 14 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>

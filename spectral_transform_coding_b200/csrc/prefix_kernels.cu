@@ -35,18 +35,17 @@
 // that the tile's barrier carries, and the exact maxima and the rescaling of O run
 // only then (always in the first tile).  l is summed in fp32 registers per thread (as a
 // third product, of P with ones, it doubles the MMAs of the tile's second half: 16
-// sequences x 32k at 12x took 49 us instead of 40, 64 x 28k at 4x no less).
+// sequences x 32k at 12x took 49 us instead of 40 when that was tried, 64 x 28k at 4x no less).
 // 8 or 16 warps do this; one more issues the MMAs and the page copies, so that neither
 // their issue time (about 50 cycles an MMA) nor the page ids' latency stands in the
 // others' way.  S of tile t + 1 is computed while tile t's scores turn into P, O of
 // tile t while the keys of tile t + 2 are unpacked.
 //
 // Bound: the issue of the unpacking and softmax instructions and the waits between the
-// phases of a tile, not HBM (4 to 10 % busy) and not the tensor cores (5 to 15 %).  This
+// phases of a tile, not HBM (3 to 9 % busy) and not the tensor cores (7 to 21 %).  This
 // kernel alone, cold: 4 sequences of 7 heads x 4 KV heads behind 128k tokens at 8x take
-// 42 us (issue slots 46 % busy), 8 x 32k at 4x 43 us, 16 x 32k at 12x 39 us, 64 x 28k at
-// 4x 96 us.  Of a tile's time the unpacking has about 43 %, the scores' way from TMEM over
-// exp2 to P 40 %.
+// 52 us (issue slots 50 % busy), 8 x 32k at 4x 48 us, 16 x 32k at 12x 47 us, 64 x 28k at
+// 4x 114 us.
 //
 // Rounding: q_lat as two fp16 parts (2^-22), which multiply the exact keys, so that a score is
 // off by 2^-22 of its |q_lat c| and by the fold's two bf16 parts of W_up (2^-16).  (With one
@@ -80,7 +79,7 @@ constexpr int kPfTok = 128;       // tokens of a tile
 constexpr int kPfMaxStages = 32;
 // p = 2^(s - m + 8), as the decode kernel's: all 11 bits down to 2^-22 of a split's largest weight,
 // nothing lost above 2^-32.  (From 2^-3 instead of 2^8 the first tile's m served longer, and 16
-// sequences x 32k at 12x took 2 us less, but weights below 2^-22 of the largest vanished from O and
+// sequences x 32k at 12x took 3 us less, but weights below 2^-22 of the largest vanished from O and
 // stayed in l: behind a first token with 0.99 of the weight and no value the output was several percent off.)
 constexpr float kPfOff = attend::kPScaleLog2;
 constexpr float kPfLimit = 15.9f;   // exponent of p above which m is taken again (fp16 ends at 2^15.999)
@@ -983,7 +982,7 @@ __global__ void __launch_bounds__(32 * W + 32, CTAS) prefix_kernel(const __grid_
 using PrefixKernel = void (*)(const PrefixArgs);
 
 // Two CTAs of 8 compute warps where shared memory holds two, else one of 16: with one CTA of
-// 8 warps 8 sequences x 32k at 4x took 63.7 us a call, with 16 warps 62.2.  Two CTAs of 16
+// 8 warps 8 sequences x 32k at 4x took 63.7 us a call, with 16 warps 62.2 (keys then in one part).  Two CTAs of 16
 // warps have 56 registers a thread, which suits 16 rows only: with 32 or 64 rows they took 78 and
 // 59 us where 8 warps took 75 and 50 (4 x 128k at 8x, 16 x 32k at 12x).
 template <int G>
